@@ -278,6 +278,147 @@ int bakron_rht(const float* X, int rows, int cols, uint64_t seed_rows, uint64_t 
 int bakron_row_scales(const float* W, int m, int n, int group_size, float divisor,
                       float* scales, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * What a rounded layer meets after the solve: its 4-bit layout, the product with the
+ * activations of a few tokens, the norm that makes 8-bit activations, and the distillation
+ * loss against the original model.
+ *
+ * Element types of the entry points below.
+ * ---------------------------------------------------------------------------------------- */
+typedef enum {
+    BAKRON_F32 = 0,
+    BAKRON_F16 = 1,
+    BAKRON_BF16 = 2,
+    BAKRON_I8 = 3,
+    BAKRON_I32 = 4,
+    BAKRON_I64 = 5
+} bakron_dtype;
+
+/* ------------------------------------------------------------------------------------------
+ * bakron_pack4 / bakron_unpack4 -- the codes and grid steps of a layer, as bakron_round_ex
+ * writes and takes them, in 4 bits a code and in the order in which bakron_matvec4 reads them.
+ *
+ * Layout: tiles of 16 rows x 64 columns, 512 bytes each; tile (i / 16, j / 64) is number
+ * (i / 16) * ceil(n / 64) + j / 64. A 32-bit word holds 8 neighbouring columns of one row, column
+ * c of the 8 in the nibble whose index is c with its three bits reversed (nibble 0 = the lowest
+ * bits), as code & 15. With r = i mod 16 and j mod 64 = 32 h + 8 t + c the word stands at byte
+ * 16 * (4 * (r mod 8) + t) + 8 * h + 4 * (r / 8) of its tile. Behind the tiles stand the grid
+ * steps, fp32, G = ceil(n / group_size) per row, in the order (row tile, group, r mod 8, r / 8).
+ * What pads the last tiles holds code 0; rows that pad the last row tile have step 0.
+ *
+ *   codes    [in/out] m x n int8, row stride ldc elements (ldc >= n).
+ *   scales   [in/out] m x G grid steps.
+ *   m, n     [in]  1 <= m, 1 <= n <= 65536, m*n < 2^31.
+ *   group_size [in] columns per grid step: a multiple of 32, or >= n (one step per row).
+ *   unsigned_codes [in] 0: codes of the integer grid, -8..7; 1: codebook indices, 0..15.
+ *   packed   [out/in] bakron_pack4_bytes(m, n, group_size) bytes, 16-B aligned.
+ *   dev_status [out] BAKRON_ERR_INVALID_ARG if a code is outside its range (its low four bits
+ *                  are stored all the same).
+ * ---------------------------------------------------------------------------------------- */
+size_t bakron_pack4_bytes(int m, int n, int group_size);
+int bakron_pack4(const int8_t* codes, int64_t ldc, const float* scales, int m, int n,
+                 int group_size, int unsigned_codes, void* packed, int* dev_status,
+                 void* stream);
+int bakron_unpack4(const void* packed, int m, int n, int group_size, int unsigned_codes,
+                   int8_t* codes, int64_t ldc, float* scales, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * bakron_matvec4 -- a layer in the layout of bakron_pack4 times the activations of one or a few
+ * tokens:
+ *
+ *   y[t][i] = sum_j s[i][j / group_size] * v(code_ij) * x[t][j]
+ *
+ * v(code) is the code itself or, with a codebook, its entry. 8-bit activations stand for
+ * x_scales[t][j / x_group_size] * x[t][j]. Products are exact or carried to 22 bits and more
+ * (fp32 activations: 24 bits; with a codebook: entries to 22 bits for fp16 and 8-bit
+ * activations, 16 for bf16, 24 for fp32), sums are fp32 (8-bit activations on the integer grid:
+ * exact within 64 columns), and the result is rounded once to y's type.
+ * Any number of tokens is right; the weights are read once for every 32 tokens (8 tokens of fp32),
+ * so it is meant for few.
+ *
+ *   packed, m, n, group_size [in] as for bakron_pack4.
+ *   codebook [in]  HOST pointer to 2^bits finite entries, copied during the call (the codes are
+ *                  then indices; entries above 2^bits count as 0); NULL selects the integer grid.
+ *   bits     [in]  1..4 with a codebook, not looked at without.
+ *   x        [in]  tokens x n, row stride ldx elements, F32, F16, BF16 or I8; any alignment its
+ *                  type allows.
+ *   x_scales [in]  tokens x ceil(n / x_group_size) fp32, for I8 only (else NULL).
+ *   x_group_size [in] a multiple of 32, or >= n (one step per token); not looked at unless I8.
+ *   tokens   [in]  0..65535; 0 does nothing.
+ *   y        [out] tokens x m, row stride ldy elements, F32, F16 or BF16.
+ * A non-finite activation makes all results of its token non-finite; whether infinite or NaN is
+ * not specified.
+ * ---------------------------------------------------------------------------------------- */
+int bakron_matvec4(const void* packed, int m, int n, int group_size, const float* codebook,
+                   int bits, const void* x, int x_dtype, int64_t ldx, const float* x_scales,
+                   int x_group_size, int tokens, void* y, int y_dtype, int64_t ldy,
+                   void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * bakron_rms_norm_q8 -- the residual's addition, the root-mean-square norm and an 8-bit output
+ * with scales (the activations of bakron_matvec4):
+ *
+ *   h = x + residual,   rho = 1 / sqrt(mean_j h_j^2 + eps),   v_j = h_j * weight_j,
+ *   scales[g] = max_{j in g} |v_j| * rho / 127,
+ *   q_j = round_half_even(127 * v_j / max_{j' in g} |v_j'|)       (0 where the maximum is 0)
+ *
+ * The codes are those of the real quotient for the given inputs: rho cancels, and a quotient
+ * near the border of two codes is decided in fp64. So q does not depend on the order of the sum.
+ *
+ *   x, residual [in] rows x n of `dtype` (F32, F16, BF16), row strides ldx, ldr; residual may be
+ *                  NULL.
+ *   weight   [in]  n of weight_dtype (F32, F16, BF16); NULL: all ones.
+ *   rows, n  [in]  rows >= 0 (0 does nothing), 1 <= n <= 65536.
+ *   eps      [in]  > 0, finite.
+ *   group_size [in] columns per scale: a multiple of 32, or >= n (one scale per row).
+ *   q        [out] rows x n int8, contiguous.
+ *   scales   [out] rows x ceil(n / group_size).
+ *   sum      [out] rows x n of `dtype`, row stride lds: h rounded to dtype; may be NULL, and may
+ *                  be the buffer of x or residual (with its stride).
+ *   dev_status [out] BAKRON_ERR_NONFINITE if a row has an h_j or v_j that is not finite in fp32;
+ *                  that row's codes are 0 and its scales NaN. May be NULL.
+ * ---------------------------------------------------------------------------------------- */
+int bakron_rms_norm_q8(const void* x, int64_t ldx, const void* residual, int64_t ldr, int dtype,
+                       const void* weight, int weight_dtype, int rows, int n, float eps,
+                       int group_size, int8_t* q, float* scales, void* sum, int64_t lds,
+                       int* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * bakron_distill -- the distillation loss from a teacher's top logits, and its gradient: the KL
+ * divergence to the original model whose second-order expansion the layer proxy is (YAQA
+ * article, sections 1 and 2). Per row, over a vocabulary of V entries and a list of k teacher entries
+ * (i_j, t_j):
+ *
+ *   q = softmax(z / tau),  lse = log sum_i exp(z_i / tau),
+ *   p_j = exp(t_j / tau - T),  T = log sum_j exp(t_j / tau), or teacher_lse (the teacher's own
+ *         log-sum-exp of t / tau over its whole vocabulary: p then sums to M <= 1),
+ *   loss = w * sum_j p_j (log p_j - log q_{i_j}),
+ *   dz_i = (w / tau) * (M q_i - sum_{j: i_j = i} p_j),   M = sum_j p_j.
+ *
+ *   logits   [in]  rows x vocab of dtype (F32, F16, BF16), row stride ld.
+ *   top_idx  [in]  rows x k of idx_dtype (I32, I64); a negative index marks an absent entry; the
+ *                  same index may stand in a row more than once.
+ *   top_logits [in] rows x k of top_dtype (F32, F16, BF16); -inf marks an absent entry.
+ *   k        [in]  1..1024.
+ *   teacher_lse [in] rows fp32, or NULL.
+ *   row_weights [in] rows fp32 w, or NULL (all 1). A row of weight 0 is not read: its loss, lse
+ *                  and gradient are 0.
+ *   temperature [in] tau > 0, finite.
+ *   loss, lse [out] rows fp32 each. A row without a present entry has loss 0 and gradient 0.
+ *   dlogits  [out] rows x vocab of dtype, row stride ldd; NULL: no gradient. May be the buffer
+ *                  of logits (with ldd = ld).
+ *   rows, vocab [in] rows >= 0 (0 does nothing), vocab >= 1.
+ *   dev_status [out] BAKRON_ERR_INVALID_ARG if an index is >= vocab (that entry counts as
+ *                  absent).
+ * Logits of -inf are entries of probability 0; a NaN, a +inf, or a row of nothing but -inf gives
+ * a row with a present entry a NaN loss and gradient.
+ * ---------------------------------------------------------------------------------------- */
+int bakron_distill(const void* logits, int dtype, int rows, int vocab, int64_t ld,
+                   const void* top_idx, int idx_dtype, const void* top_logits, int top_dtype,
+                   int k, const float* teacher_lse, const float* row_weights, float temperature,
+                   float* loss, float* lse, void* dlogits, int64_t ldd, int* dev_status,
+                   void* stream);
+
 /* Synchronises `stream`, then returns the device status word (a bakron_status value), or
  * BAKRON_ERR_CUDA if the synchronisation itself failed. */
 int bakron_read_status(const int* dev_status, void* stream);
@@ -289,8 +430,8 @@ const char* bakron_status_string(int code);
  * (diagnostics: lets a benchmark count its launches). */
 unsigned long long bakron_kernel_launches(void);
 
-/* Library version as 10000*major + 100*minor + patch (0.2.0: stochastic Q, the pluggable
- * base quantizer, the Kronecker-factor and incoherence-processing entry points). */
+/* Library version as 10000*major + 100*minor + patch (0.3.0: the 4-bit layout and its
+ * product, the 8-bit norm and the distillation loss). */
 int bakron_version(void);
 
 #ifdef __cplusplus

@@ -4,3 +4,4 @@ Only the tests, the smoke check and the CPU-baseline leg of the benchmark may im
 package. It shares no code with the CUDA library.
 """
 from .bakron_oracle import *  # noqa: F401,F403
+from .packed_oracle import *  # noqa: F401,F403

@@ -2,12 +2,14 @@
 
 The functions named like the C ABI (``bakron_ldl``, ``bakron_round``,
 ``bakron_round_stochastic``, ``bakron_round_ex``, ``bakron_proxy_loss``, ``bakron_damped_gram``,
-``bakron_sketch_b``, ``bakron_rht``, ``bakron_row_scales``, ``bakron_read_status``,
+``bakron_sketch_b``, ``bakron_rht``, ``bakron_row_scales``, ``bakron_pack4``, ``bakron_unpack4``,
+``bakron_matvec4``, ``bakron_rms_norm_q8``, ``bakron_distill``, ``bakron_read_status``,
 ``bakron_status_string`` and the ``*_workspace_bytes`` queries) take torch CUDA tensors, pass
 their device pointers and the current CUDA stream to the library and return its status code.
 ``ldl``, ``round_weights``, ``proxy_loss``, ``damped_gram``, ``sketch_b``, ``rht``,
-``row_scales`` and ``solve`` additionally allocate outputs and workspaces with torch and raise
-on any error.
+``row_scales``, ``pack4``, ``unpack4``, ``matvec4``, ``rms_norm_q8``, ``distill`` and ``solve``
+additionally allocate outputs and workspaces with torch and raise on any error. ``PackedLayer``
+keeps a rounded layer in 4 bits.
 
 Every step of the computation runs in the library's CUDA kernels; there is no CPU path. If
 the shared library is missing the first call raises.
@@ -34,7 +36,12 @@ BAKRON_ERR_WORKSPACE = -5
 BAKRON_ERR_NONFINITE = -6
 BAKRON_ERR_CAPTURE = -7
 
+# bakron_dtype
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3, torch.int32: 4,
+           torch.int64: 5}
+
 _c_size_t, _c_int, _vp = ctypes.c_size_t, ctypes.c_int, ctypes.c_void_p
+_i64 = ctypes.c_int64
 _SIGNATURES = {
     "bakron_ldl_workspace_bytes": (_c_size_t, [_c_int]),
     "bakron_ldl": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _c_size_t, _vp, _vp]),
@@ -58,6 +65,15 @@ _SIGNATURES = {
     "bakron_rht": (_c_int, [_vp, _c_int, _c_int, ctypes.c_uint64, ctypes.c_uint64, _c_int, _vp,
                             _vp, _c_size_t, _vp]),
     "bakron_row_scales": (_c_int, [_vp, _c_int, _c_int, _c_int, ctypes.c_float, _vp, _vp]),
+    "bakron_pack4_bytes": (_c_size_t, [_c_int, _c_int, _c_int]),
+    "bakron_pack4": (_c_int, [_vp, _i64, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
+    "bakron_unpack4": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _vp, _i64, _vp, _vp]),
+    "bakron_matvec4": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _c_int, _i64, _vp,
+                                _c_int, _c_int, _vp, _c_int, _i64, _vp]),
+    "bakron_rms_norm_q8": (_c_int, [_vp, _i64, _vp, _i64, _c_int, _vp, _c_int, _c_int, _c_int,
+                                    ctypes.c_float, _c_int, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "bakron_distill": (_c_int, [_vp, _c_int, _c_int, _c_int, _i64, _vp, _c_int, _vp, _c_int,
+                                _c_int, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _i64, _vp, _vp]),
     "bakron_read_status": (_c_int, [_vp, _vp]),
     "bakron_status_string": (ctypes.c_char_p, [_c_int]),
     "bakron_version": (_c_int, []),
@@ -267,6 +283,185 @@ def bakron_row_scales(W, group_size, divisor, scales, stream=None) -> int:
                                    _stream(stream))
 
 
+# The entry points below are called once a layer and token, so their binding is kept short: sizes
+# and strides are read once, the library checks them, and only what it cannot see (device, type,
+# a strided last dimension, the length of a buffer) is checked here.
+def _rows(t: torch.Tensor, name: str):
+    """(rows, columns, row stride) of a 1-D or 2-D CUDA tensor whose last stride is 1."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() == 1:
+        if t.numel() > 1 and t.stride(0) != 1:
+            raise ValueError(f"{name}: the last dimension must have stride 1")
+        return 1, t.shape[0], t.shape[0]
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected one or two dimensions, got {tuple(t.shape)}")
+    r, c = t.shape
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the last dimension must have stride 1")
+    ld = t.stride(0) if r > 1 else c
+    if ld < c:
+        raise ValueError(f"{name}: rows must not overlap")
+    return r, c, ld
+
+
+def _flat(t, dtype, numel: int, name: str, device) -> int:
+    """Data pointer of a contiguous tensor of a given type and length on ``device``."""
+    if t.dtype != dtype or t.numel() != numel or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {numel} contiguous {dtype} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} on "
+                         f"{t.device}")
+    return t.data_ptr()
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name}: unsupported type {t.dtype}")
+    return d
+
+
+def _call(fn, device, stream, *args) -> int:
+    """fn(*args, stream) with ``device`` current: the library launches on the current device."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        st = _raw_stream(i) if stream is None else _stream(stream)
+        return fn(*args, st)
+    with torch.cuda.device(i):
+        return fn(*args, _raw_stream(i) if stream is None else _stream(stream))
+
+
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+def _steps(n: int, group_size) -> tuple[int, int]:
+    """(columns per step, steps per row); None is one step per row."""
+    g = n if group_size is None else int(group_size)
+    if g < 1:
+        raise ValueError(f"group_size must be positive, got {group_size}")
+    return g, (1 if g >= n else -(-n // g))
+
+
+def _codebook(codebook):
+    """(ctypes array or None, bits) of a host codebook of 2, 4, 8 or 16 entries."""
+    if codebook is None:
+        return None, 0
+    if not isinstance(codebook, ctypes.Array):
+        codebook = (ctypes.c_float * len(codebook))(*[float(v) for v in codebook])
+    bits = len(codebook).bit_length() - 1
+    if len(codebook) != 1 << bits or not 1 <= bits <= 4:
+        raise ValueError(f"a codebook has 2, 4, 8 or 16 entries, got {len(codebook)}")
+    return codebook, bits
+
+
+def bakron_pack4_bytes(m: int, n: int, group_size: int) -> int:
+    return int(lib().bakron_pack4_bytes(int(m), int(n), int(group_size)))
+
+
+def bakron_pack4(codes, scales, group_size, unsigned_codes, packed, dev_status,
+                 stream=None) -> int:
+    m, n, ldc = _rows(codes, "codes")
+    if codes.dtype != torch.int8:
+        raise ValueError(f"codes: expected torch.int8, got {codes.dtype}")
+    dev = codes.device
+    g, G = _steps(n, group_size)
+    return _call(lib().bakron_pack4, dev, stream, codes.data_ptr(), ldc,
+                 _flat(scales, torch.float32, m * G, "scales", dev), m, n, g,
+                 int(bool(unsigned_codes)),
+                 _flat(packed, torch.uint8, bakron_pack4_bytes(m, n, g), "packed", dev),
+                 _flat(dev_status, torch.int32, 1, "dev_status", dev))
+
+
+def bakron_unpack4(packed, group_size, unsigned_codes, codes, scales, stream=None) -> int:
+    m, n, ldc = _rows(codes, "codes")
+    if codes.dtype != torch.int8:
+        raise ValueError(f"codes: expected torch.int8, got {codes.dtype}")
+    dev = codes.device
+    g, G = _steps(n, group_size)
+    return _call(lib().bakron_unpack4, dev, stream,
+                 _flat(packed, torch.uint8, bakron_pack4_bytes(m, n, g), "packed", dev), m, n, g,
+                 int(bool(unsigned_codes)), codes.data_ptr(), ldc,
+                 _flat(scales, torch.float32, m * G, "scales", dev))
+
+
+def bakron_matvec4(packed, group_size, codebook, x, x_scales, x_group_size, y,
+                   stream=None) -> int:
+    """``x``: tokens x n (or n), ``y``: tokens x m (or m); ``codebook``: None, a sequence or a
+    ctypes float array."""
+    tokens, n, ldx = _rows(x, "x")
+    rows, m, ldy = _rows(y, "y")
+    dev = x.device
+    if rows != tokens or y.device != dev:
+        raise ValueError(f"y: expected {tokens} rows on {dev}, got {tuple(y.shape)} on {y.device}")
+    g, _ = _steps(n, group_size)
+    L = lib()
+    nbytes = L.bakron_pack4_bytes(m, n, g)
+    if nbytes == 0:
+        return BAKRON_ERR_INVALID_ARG
+    cb, bits = _codebook(codebook)
+    gx, xs = n, None
+    if x_scales is not None:
+        gx, Gx = _steps(n, x_group_size)
+        xs = _flat(x_scales, torch.float32, tokens * Gx, "x_scales", dev)
+    return _call(L.bakron_matvec4, dev, stream, _flat(packed, torch.uint8, nbytes, "packed", dev),
+                 m, n, g, cb, bits, x.data_ptr(), _dtype(x, "x"), ldx, xs, gx, tokens,
+                 y.data_ptr(), _dtype(y, "y"), ldy)
+
+
+def bakron_rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out=None,
+                       dev_status=None, stream=None) -> int:
+    rows, n, ldx = _rows(x, "x")
+    dev = x.device
+    g, G = _steps(n, group_size)
+    ldr = lds = 0
+    rp = wp = sp = None
+    wd = 0
+    if residual is not None:
+        rr, rn, ldr = _rows(residual, "residual")
+        if (rr, rn) != (rows, n) or residual.dtype != x.dtype or residual.device != dev:
+            raise ValueError("residual: expected the shape, type and device of x")
+        rp = residual.data_ptr()
+    if sum_out is not None:
+        sr, sn, lds = _rows(sum_out, "sum_out")
+        if (sr, sn) != (rows, n) or sum_out.dtype != x.dtype or sum_out.device != dev:
+            raise ValueError("sum_out: expected the shape, type and device of x")
+        sp = sum_out.data_ptr()
+    if weight is not None:
+        wp = _flat(weight, weight.dtype, n, "weight", dev)
+        wd = _dtype(weight, "weight")
+    st = None if dev_status is None else _flat(dev_status, torch.int32, 1, "dev_status", dev)
+    return _call(lib().bakron_rms_norm_q8, dev, stream, x.data_ptr(), ldx, rp, ldr,
+                 _dtype(x, "x"), wp, wd, rows, n, float(eps), g,
+                 _flat(q, torch.int8, rows * n, "q", dev),
+                 _flat(scales, torch.float32, rows * G, "scales", dev), sp, lds, st)
+
+
+def bakron_distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature, loss, lse,
+                   dlogits, dev_status, stream=None) -> int:
+    rows, V, ld = _rows(logits, "logits")
+    dev = logits.device
+    k = top_idx.shape[-1]
+    ldd, dp = 0, None
+    if dlogits is not None:
+        dr, dv, ldd = _rows(dlogits, "dlogits")
+        if (dr, dv) != (rows, V) or dlogits.dtype != logits.dtype or dlogits.device != dev:
+            raise ValueError("dlogits: expected the shape, type and device of logits")
+        dp = dlogits.data_ptr()
+    return _call(lib().bakron_distill, dev, stream, logits.data_ptr(), _dtype(logits, "logits"),
+                 rows, V, ld, _flat(top_idx, top_idx.dtype, rows * k, "top_idx", dev),
+                 _dtype(top_idx, "top_idx"),
+                 _flat(top_logits, top_logits.dtype, rows * k, "top_logits", dev),
+                 _dtype(top_logits, "top_logits"), k,
+                 None if teacher_lse is None else
+                 _flat(teacher_lse, torch.float32, rows, "teacher_lse", dev),
+                 None if row_weights is None else
+                 _flat(row_weights, torch.float32, rows, "row_weights", dev),
+                 float(temperature), _flat(loss, torch.float32, rows, "loss", dev),
+                 _flat(lse, torch.float32, rows, "lse", dev), dp, ldd,
+                 _flat(dev_status, torch.int32, 1, "dev_status", dev))
+
+
 def internal_hadamard28():
     """The order-28 Hadamard matrix the library's transform uses (host construction)."""
     import numpy as np
@@ -430,6 +625,118 @@ def proxy_loss(dW, H_O, H_I, stream=None) -> torch.Tensor:
     return loss
 
 
+def _status_of(status, device, check: bool):
+    """(status word, whether to read it): the caller's own word is left to the caller."""
+    return (new_status(device), check) if status is None else (status, False)
+
+
+def pack4(codes, scales, group_size=None, unsigned: bool = False, stream=None,
+          check: bool = True, status=None) -> torch.Tensor:
+    """The 4-bit layout of a layer's codes (m x n int8) and grid steps (m, or m x G with a
+    group size); ``unsigned`` for codebook indices. With the caller's own ``status`` word the
+    call does not wait for the device."""
+    m, n, _ = _rows(codes, "codes")
+    g, _ = _steps(n, group_size)
+    nbytes = bakron_pack4_bytes(m, n, g)
+    if nbytes == 0:
+        raise BakronError(BAKRON_ERR_INVALID_ARG, "bakron_pack4")
+    packed = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+    st, read = _status_of(status, codes.device, check)
+    _raise(bakron_pack4(codes, scales, g, unsigned, packed, st, stream), "bakron_pack4")
+    if read:
+        _raise(bakron_read_status(st, stream), "bakron_pack4 (device)")
+    return packed
+
+
+def unpack4(packed, m: int, n: int, group_size=None, unsigned: bool = False, stream=None):
+    """(codes, scales) of a layer in the 4-bit layout; scales m, or m x G with a group size."""
+    _, G = _steps(n, group_size)
+    codes = torch.empty((m, n), dtype=torch.int8, device=packed.device)
+    scales = torch.empty((m,) if group_size is None else (m, G), dtype=torch.float32,
+                         device=packed.device)
+    _raise(bakron_unpack4(packed, group_size, unsigned, codes, scales, stream), "bakron_unpack4")
+    return codes, scales
+
+
+def matvec4(packed, m: int, n: int, x, group_size=None, codebook=None, x_scales=None,
+            x_group_size=None, out_dtype=None, stream=None) -> torch.Tensor:
+    """y = x W^T for a layer (m x n) in the 4-bit layout and x of one token (n) or a few (tokens x
+    n); y has x's type (float32 for int8 x) unless ``out_dtype`` names another."""
+    if x.shape[-1] != n:
+        raise ValueError(f"x: expected {n} columns, got {tuple(x.shape)}")
+    if out_dtype is None:
+        out_dtype = torch.float32 if x.dtype == torch.int8 else x.dtype
+    y = torch.empty(x.shape[:-1] + (m,), dtype=out_dtype, device=x.device)
+    _raise(bakron_matvec4(packed, group_size, codebook, x, x_scales, x_group_size, y, stream),
+           "bakron_matvec4")
+    return y
+
+
+def rms_norm_q8(x, weight=None, eps: float = 1e-6, residual=None, group_size=None, sum_out=None,
+                status=None, stream=None):
+    """(q int8, scales, sum): the norm of x + residual in 8 bits, and the sum in x's type (None
+    without a residual, unless ``sum_out`` asks for it). Scales: one per row, or rows x G with a
+    group size. Rows that are not finite give NaN scales and, where the caller gives a ``status``
+    word, BAKRON_ERR_NONFINITE in it."""
+    n = x.shape[-1]
+    _, G = _steps(n, group_size)
+    lead = x.shape[:-1]
+    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    scales = torch.empty(lead + (G,), dtype=torch.float32, device=x.device)
+    if sum_out is None and residual is not None:
+        sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _raise(bakron_rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out, status,
+                              stream), "bakron_rms_norm_q8")
+    return q, scales, sum_out
+
+
+def distill(logits, top_idx, top_logits, temperature: float = 1.0, teacher_lse=None,
+            row_weights=None, grad: bool = True, dlogits=None, stream=None, check: bool = True,
+            status=None):
+    """(loss, lse, dlogits) of the distillation from a teacher's top logits: per-row weighted KL,
+    the student's log-sum-exp of logits / temperature, and the gradient of the summed loss (None
+    unless ``grad``; ``dlogits`` names its buffer, which may be ``logits``). With the caller's own
+    ``status`` word the call does not wait for the device."""
+    rows = 1 if logits.dim() == 1 else logits.shape[0]
+    loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    lse = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    if not grad:
+        dlogits = None
+    elif dlogits is None:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    st, read = _status_of(status, logits.device, check)
+    _raise(bakron_distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature,
+                          loss, lse, dlogits, st, stream), "bakron_distill")
+    if read:
+        _raise(bakron_read_status(st, stream), "bakron_distill (device)")
+    return loss, lse, dlogits
+
+
+class PackedLayer:
+    """A rounded layer kept in 4 bits: what ``Solver.run`` or ``round_weights`` left in ``codes``,
+    with its grid steps and, where the round took one, its codebook.
+
+        layer = bk.PackedLayer(codes, scales, group_size=128)
+        y = layer.matvec(x)                           # x: n, or tokens x n
+        y = layer.matvec(q, x_scales=s)               # the int8 output of rms_norm_q8
+    """
+
+    def __init__(self, codes, scales, group_size=None, codebook=None, stream=None):
+        self.m, self.n = codes.shape
+        self.group_size = group_size
+        self.codebook, _ = _codebook(codebook)
+        self.packed = pack4(codes, scales, group_size, codebook is not None, stream)
+
+    def matvec(self, x, x_scales=None, x_group_size=None, out_dtype=None, stream=None):
+        return matvec4(self.packed, self.m, self.n, x, self.group_size, self.codebook, x_scales,
+                       x_group_size, out_dtype, stream)
+
+    def unpack(self, stream=None):
+        """(codes, scales) as they were given."""
+        return unpack4(self.packed, self.m, self.n, self.group_size, self.codebook is not None,
+                       stream)
+
+
 class Solver:
     """Reusable buffers for the whole path: ldl(H_O), ldl(H_I), round, proxy loss.
 
@@ -453,6 +760,7 @@ class Solver:
                                 bakron_proxy_loss_workspace_bytes(m, n)), self.device)
         self.E = self.ws_round[: 4 * m * n].view(torch.float32).view(m, n)
         self._rot = None     # incoherence buffers, made on first use
+        self._steps = None   # (scales, group_size, codebook) of the last run
         self.status = new_status(self.device)
         # the two factorisations are independent: ldl(H_O) runs on a side stream while
         # ldl(H_I) runs on the caller's stream
@@ -530,6 +838,7 @@ class Solver:
         else:
             call("round", stream, bakron_round_stochastic, Wstar, self.L_O, self.L_I, scales,
                  bits, seed, self.codes, self.W, self.ws_round, self.status)
+        self._steps = (scales, group_size, codebook)
         if with_loss:
             call("loss", stream, bakron_proxy_loss, self.E, H_O, H_I, self.loss, self.ws)
         if incoherence is not None:
@@ -544,6 +853,14 @@ class Solver:
 
     def check(self, stream=None):
         _raise(bakron_read_status(self.status, stream), "bakron (device)")
+
+    def packed(self, stream=None) -> PackedLayer:
+        """The layer that the last ``run`` rounded, in 4 bits (for bits <= 4), with the grid steps,
+        group size and codebook of that run. After a run with ``incoherence`` it is the rotated
+        layer W~."""
+        if self._steps is None:
+            raise ValueError("no layer was rounded yet")
+        return PackedLayer(self.codes, *self._steps, stream)
 
 
 def solve(Wstar, H_O, H_I, scales, bits, stream=None, seed=None):

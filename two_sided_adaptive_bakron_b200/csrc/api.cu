@@ -51,4 +51,4 @@ extern "C" const char* bakron_status_string(int code) {
     }
 }
 
-extern "C" int bakron_version(void) { return 200; }
+extern "C" int bakron_version(void) { return 300; }
