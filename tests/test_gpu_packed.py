@@ -420,3 +420,10 @@ def test_streams_capture_and_replay(bk):
         ref = step()
         assert all(torch.equal(a, b) for a, b in zip(o1, ref))
         assert all(torch.equal(a, b) for a, b in zip(o2, ref))
+
+
+@pytest.mark.parametrize("x", ["f32", "f16", "bf16", "i8"])
+@pytest.mark.parametrize("book", [None, BOOK16])
+def test_product_of_the_longest_rows(bk, x, book):
+    """Activations that fill shared memory: fewer tokens a block."""
+    _check_product(bk, 20, 65536, 9, x, "f32", 32, book, x_group=32 if x == "i8" else None, seed=2)

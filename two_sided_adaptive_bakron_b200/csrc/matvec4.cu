@@ -12,9 +12,11 @@
 // same. (tcgen05.mma would want the unpacked weights in shared memory first: two more passes over
 // them there, for products that are not what bounds this kernel.)
 //
-//   * A warp owns a row tile (16 rows) and a slice of the columns. Its loads are the layout's 512-byte
-//     tiles, 16 bytes a lane, four tiles ahead of their use, in registers: each lane's 16 bytes are its
-//     own fragments of four m16n8k16 (two m16n8k32) products.
+//   * A warp owns a row tile (16 rows) and a slice of the columns. Each lane's 16 bytes of a 512-byte
+//     tile are its own fragments of four m16n8k16 (two m16n8k32) products. A warp copies its tiles
+//     and their steps into a ring of its own in shared memory with cp.async, a stage of eight tiles
+//     ahead of the one in use: nothing waits for another warp, and 24 warps keep 96 KB an SM in flight
+//     without registers.
 //   * The codes become f16 or bf16 by setting the exponent bits around them (1024 + code and
 //     128 + code are exact) and one subtraction a pair; int8 by masking: a code in the upper half of
 //     its byte is 16 times the code. fp32 activations are split in three bf16 parts of 8 bits, which
@@ -28,19 +30,19 @@
 //     distributed shared memory in rank order: no atomics, the same bits every time.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
 #include "pack4.cuh"
+#include "tcgemm_host.cuh"
 
 namespace bakron {
 namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kAhead = 4;          // column tiles a warp loads ahead
+constexpr int kStages = 2;
 
 enum Kind { kF16, kBf16, kF32, kI8, kF16Book, kBf16Book, kF32Book };
 constexpr bool is_book(int k) { return k >= kF16Book; }
@@ -51,6 +53,12 @@ constexpr bool is_half(int k) { return k == kF16 || k == kF16Book; }
 constexpr int tile_tokens(int k) { return is_split(k) ? 2 : 8; }
 constexpr int token_rows(int k) { return is_split(k) ? 3 : 1; }
 
+// Stages, warps of a block and blocks of an SM: 16 warps an SM, which share one table of codebook
+// pairs (64 to 96 KB) where there is one.
+constexpr int batch_of(int k) { return is_book(k) ? 4 : 8; }   // column tiles of a stage
+constexpr int warps_of(int k) { return is_book(k) ? 16 : 8; }
+constexpr int blocks_of(int k) { return is_book(k) ? 1 : 2; }
+
 struct Book { uint32_t part[3][16]; };   // 16-bit parts of the entries (host-made)
 
 struct Args {
@@ -58,42 +66,60 @@ struct Args {
     const void* x; int x_dtype; int64_t ldx; const float* xs; int Gx, gx;
     int tokens; void* y; int y_dtype; int64_t ldy;
     int slice;               // column tiles of a block
-    int tpw;                 // row tiles of a warp
+    int batch_groups;        // groups that kBatch tiles may touch
+    int step_shift;          // kPerTile: column tile u of a batch takes step u >> step_shift
+    int batch_gq, batch_gr;  // columns of kBatch tiles in whole groups and the rest
+    int clusters;            // the row tiles are dealt out over so many clusters of blocks
+    int tiles_each, tiles_rest;   // so many row tiles each, and one more for the first few
+    int max_tiles;           // the most that one of them gets
+    int chunk;               // tokens of a block
     int pitch;               // bytes between staged rows of x
     float out1, out2;        // powers of two for the result
     Book book;
 };
 
-__device__ __forceinline__ uint4 load_tile(const uint4* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Copies 16 bytes, or fills them with zeros.
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// d = a b + c
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
+                                        uint32_t b1, const float (&c)[4]) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
+                                         uint32_t b1, const float (&c)[4]) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                       uint32_t b1) {
+                                       uint32_t b1, const int (&c)[4]) {
     asm volatile(
         "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{%10,%11,%12,%13};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]),
+          "r"(c[2]), "r"(c[3]));
 }
 
 // (w & mask) ^ bits
@@ -103,7 +129,7 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t 
     return r;
 }
 
-// The 8 codes of a word as four f16 pairs: columns (0, 1), (4, 5), (2, 3), (6, 7). The xor turns
+// The 8 codes of a word as four f16 pairs: columns (0, 1), (2, 3), (4, 5), (6, 7). The xor turns
 // the two's complement nibble into code + 8 under the exponent of 1024 (or 64 for the upper
 // nibble, with the product by 1/16).
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&p)[4]) {
@@ -111,11 +137,11 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&p)[4]) {
     const __half2 c1 = __floats2half2_rn(-72.f, -72.f), r16 = __floats2half2_rn(0.0625f, 0.0625f);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const uint32_t u = q < 2 ? w : w >> 8;
-        const uint32_t v = (q & 1) ? and_xor(u, 0x00F000F0u, 0x64806480u)
-                                   : and_xor(u, 0x000F000Fu, 0x64086408u);
+        const uint32_t u = q & 1 ? w >> 8 : w;
+        const uint32_t v = q & 2 ? and_xor(u, 0x00F000F0u, 0x64806480u)
+                                 : and_xor(u, 0x000F000Fu, 0x64086408u);
         __half2 h = *reinterpret_cast<const __half2*>(&v);
-        h = (q & 1) ? __hfma2(h, r16, c1) : __hsub2(h, c0);
+        h = q & 2 ? __hfma2(h, r16, c1) : __hsub2(h, c0);
         p[q] = *reinterpret_cast<uint32_t*>(&h);
     }
 }
@@ -124,7 +150,8 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t (&p)[4]) {
     const __nv_bfloat162 c = __floats2bfloat162_rn(136.f, 136.f);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const uint32_t v = and_xor(w >> (4 * q), 0x000F000Fu, 0x43084308u);
+        const int nib = (q & 1) * 2 + (q >> 1);
+        const uint32_t v = and_xor(w >> (4 * nib), 0x000F000Fu, 0x43084308u);
         const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), c);
         p[q] = *reinterpret_cast<const uint32_t*>(&h);
     }
@@ -162,116 +189,168 @@ __device__ __forceinline__ void split3(float v, uint32_t (&h)[3]) {
     }
 }
 
-// Copies columns [j0, j0 + 8 chunks) of tokens [t0, t0 + count) to shared memory, in the type and the
-// order within 8 columns that the products take.
+// Copies columns [j0, j0 + 64 tiles) of tokens [t0, t0 + count) to shared memory as the products
+// take them: 16-bit and 8-bit activations as they are (asynchronously where their rows are aligned),
+// int8 as f16 for a codebook, fp32 in its three parts. Columns from n on are zeros.
 template <int K, class X>
 __device__ __forceinline__ void stage_x(char* sx, const Args& a, int t0, int count, int j0,
-                                        int chunks) {
-    const X* x = static_cast<const X*>(a.x);
-    const bool wide = a.ldx * sizeof(X) % 16 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
-    for (int e = threadIdx.x; e < count * chunks; e += kThreads) {
-        const int t = e / chunks, q = e - t * chunks, j = j0 + 8 * q;
-        __align__(16) X v[8];
-        load8<X>(x + (int64_t)(t0 + t) * a.ldx + j, a.n - j, wide, v);
-        if constexpr (K == kI8) {
-            // bytes in the order of the masked nibbles; a tile's two halves of a lane side by side
-            const uint2 u = *reinterpret_cast<const uint2*>(v);
-            char* dst = sx + t * a.pitch + (q / 8) * 64 + (q % 4) * 16 + (q / 4 % 2) * 8;
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(__byte_perm(u.x, 0, 0x3120), __byte_perm(u.y, 0, 0x3120));
-        } else {
-            uint32_t h[3][8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if constexpr (is_split(K)) {
-                    uint32_t s[3];
-                    split3(v[c], s);
-                    h[0][c] = s[0], h[1][c] = s[1], h[2][c] = s[2];
-                } else if constexpr (std::is_same<X, int8_t>::value) {
-                    h[0][c] = __half_as_ushort(__int2half_rn(v[c]));
+                                        int tiles) {
+    constexpr int kThreads = warps_of(K) * 32;
+    const X* x = static_cast<const X*>(a.x) + (int64_t)t0 * a.ldx;
+    const bool wide = a.ldx * sizeof(X) % 16 == 0 &&
+                      reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
+    if constexpr (!is_split(K) && !(K == kF16Book && std::is_same<X, int8_t>::value)) {
+        constexpr int per = 16 / sizeof(X);
+        const int chunks = tiles * 64 / per;
+        for (int t = 0; t < count; ++t) {
+            const X* row = x + (int64_t)t * a.ldx;
+            char* dst = sx + t * a.pitch;
+            for (int q = threadIdx.x; q < chunks; q += kThreads) {
+                const int j = j0 + per * q;
+                if (wide && j + per <= a.n) {
+                    copy16((uint32_t)__cvta_generic_to_shared(dst + 16 * q), row + j);
                 } else {
-                    h[0][c] = *reinterpret_cast<const uint16_t*>(&v[c]);
+                    __align__(16) X v[per];
+                    memset(v, 0, sizeof v);
+#pragma unroll
+                    for (int c = 0; c < per; ++c)
+                        if (j + c < a.n) v[c] = row[j + c];
+                    *reinterpret_cast<uint4*>(dst + 16 * q) = *reinterpret_cast<const uint4*>(v);
                 }
             }
+        }
+    } else {
+        const int chunks = tiles * 8;
+        for (int t = 0; t < count; ++t) {
+            const X* row = x + (int64_t)t * a.ldx;
+#pragma unroll 2
+            for (int q = threadIdx.x; q < chunks; q += kThreads) {
+                const int j = j0 + 8 * q;
+                __align__(16) X v[8];
+                load8<X>(row + j, a.n - j, wide, v);
+                uint32_t h[3][8];
 #pragma unroll
-            for (int s = 0; s < token_rows(K); ++s) {
-                uint4 o;
-                if constexpr (is_book(K))     // pairs as the table gives them
-                    o = make_uint4(h[s][0] | h[s][4] << 16, h[s][2] | h[s][6] << 16,
-                                   h[s][1] | h[s][5] << 16, h[s][3] | h[s][7] << 16);
-                else                          // first and second product's pairs
-                    o = make_uint4(h[s][0] | h[s][1] << 16, h[s][4] | h[s][5] << 16,
-                                   h[s][2] | h[s][3] << 16, h[s][6] | h[s][7] << 16);
-                *reinterpret_cast<uint4*>(sx + (t * token_rows(K) + s) * a.pitch + q * 16) = o;
+                for (int c = 0; c < 8; ++c) {
+                    if constexpr (is_split(K)) {
+                        uint32_t s[3];
+                        split3(v[c], s);
+                        h[0][c] = s[0], h[1][c] = s[1], h[2][c] = s[2];
+                    } else {
+                        h[0][c] = __half_as_ushort(__int2half_rn(v[c]));
+                    }
+                }
+#pragma unroll
+                for (int s = 0; s < token_rows(K); ++s)
+                    *reinterpret_cast<uint4*>(sx + (t * token_rows(K) + s) * a.pitch + q * 16) =
+                        make_uint4(h[s][0] | h[s][1] << 16, h[s][2] | h[s][3] << 16,
+                                   h[s][4] | h[s][5] << 16, h[s][6] | h[s][7] << 16);
             }
         }
     }
 }
 
-// K: kind, NT: 8-column tiles of the product, HALF: steps change every 32 columns.
-template <int K, int NT, bool HALF>
-__global__ void __launch_bounds__(kThreads, 2) matvec4_kernel(const __grid_constant__ Args a) {
-    constexpr int kTok = NT * tile_tokens(K);
-    constexpr int kFlush = HALF ? 2 : 1;
+// Where the steps change: never within a batch, every 1, 2 or 4 column tiles of it, or anywhere
+// (at multiples of 32 columns).
+enum Steps { kPerBatch, kPerTile, kAnywhere };
+
+// K: kind, NT: 8-column tiles of the product.
+template <int K, int NT, int STEPS>
+__global__ void __launch_bounds__(warps_of(K) * 32, blocks_of(K))
+matvec4_kernel(const __grid_constant__ Args a) {
+    constexpr int kTok = NT * tile_tokens(K), kBatch = batch_of(K);
+    constexpr bool HALF = STEPS == kAnywhere;
+    constexpr int kWarps = warps_of(K), kThreads = kWarps * 32;
     extern __shared__ __align__(128) char smem[];
+    __shared__ int head_tile[kWarps];      // the tile that a warp ends but did not begin
     cg::cluster_group cluster = cg::this_cluster();
     const int ck = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
+    const int lane = threadIdx.x & 31, g = lane / 4, t = lane % 4;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);   // uniform
     const Pack4Shape P(a.m, a.n, a.G);
-    const int kt0 = rank * a.slice, kt1 = min(P.kt, kt0 + a.slice);
-    const int block = blockIdx.x / ck;
-    const int rt_first = block * kWarps * a.tpw + warp;
-    const int t0 = blockIdx.y * kTok, count = min(kTok, a.tokens - t0);
+    const int kt0 = min(P.kt, rank * a.slice), kt1 = min(P.kt, kt0 + a.slice);
+    const int cl = blockIdx.x / ck;
+    const int rt0 = cl * a.tiles_each + min(cl, a.tiles_rest);
+    const int rt1 = rt0 + a.tiles_each + (cl < a.tiles_rest);
+    const int batches = (kt1 - kt0 + kBatch - 1) / kBatch;
+    const int t0 = blockIdx.y * a.chunk, count = min(a.chunk, a.tokens - t0);
 
-    char* sx = smem;
-    char* at = smem + kTok * token_rows(K) * a.pitch;
+    // stages of this warp: kBatch tiles, then the steps of their groups
+    const int stage_bytes = kBatch * 512 + a.batch_groups * 64;
+    char* ring = smem + warp * kStages * stage_bytes;
+    char* sx = smem + kWarps * kStages * stage_bytes;
+    char* at = sx + a.chunk * token_rows(K) * a.pitch;
     const uint32_t* table = reinterpret_cast<const uint32_t*>(at);
     if constexpr (is_book(K)) at += planes(K) * 32768;
-    float* part = reinterpret_cast<float*>(at);           // [kTok][rows of the block]
-    const int rows = kWarps * a.tpw * 16;
-    float* sxs = part + kTok * rows;                      // [kTok][steps of x in the slice]
+    const int rows = a.max_tiles * 16;
+    float* part = reinterpret_cast<float*>(at);           // [kTok][rows]
+    float* head = part + kTok * rows;                     // [warp][kTok][16]
+    float* sxs = head + kWarps * kTok * 16;               // [kTok][steps of x in the slice]
     const int xg0 = a.Gx > 1 ? kt0 * 64 / a.gx : 0;
 
-    const uint4* tiles = reinterpret_cast<const uint4*>(a.packed) + lane;
-    const float2* steps = reinterpret_cast<const float2*>(a.packed + P.code_bytes()) + g;
+    if constexpr (K == kF32 || K == kF32Book) {
+        stage_x<K, float>(sx, a, t0, count, kt0 * 64, batches * kBatch);
+    } else if constexpr (K == kF16) {
+        stage_x<K, __half>(sx, a, t0, count, kt0 * 64, batches * kBatch);
+    } else if constexpr (K == kI8) {
+        stage_x<K, int8_t>(sx, a, t0, count, kt0 * 64, batches * kBatch);
+    } else if constexpr (K == kF16Book) {
+        if (a.x_dtype == BAKRON_I8) stage_x<K, int8_t>(sx, a, t0, count, kt0 * 64, batches * kBatch);
+        else stage_x<K, __half>(sx, a, t0, count, kt0 * 64, batches * kBatch);
+    } else {
+        stage_x<K, __nv_bfloat16>(sx, a, t0, count, kt0 * 64, batches * kBatch);
+    }
+    copy_commit();
 
-    // the first tiles are on their way before x is staged
-    uint4 cur[kAhead], nxt[kAhead];
-    float2 scur[kAhead][kFlush], snxt[kAhead][kFlush];
-    auto fetch = [&](int rt, int kt, uint4 (&w)[kAhead], float2 (&s)[kAhead][kFlush]) {
+    // The block's batches, row tile after row tile, are dealt out evenly over its warps. All of
+    // a warp's steps commit a group, those without work an empty one, so that the waits count alike.
+    const int units = (rt1 - rt0) * batches;
+    const int u0 = units * warp / kWarps;
+    const int u1 = units * (warp + 1) / kWarps;
+    const int first_tile = batches > 0 ? rt0 + u0 / batches : 0;
+    const int first_batch = batches > 0 ? u0 % batches : 0;
+    const uint32_t ring32 = (uint32_t)__cvta_generic_to_shared(ring) + lane * 16;
+
+    // where the next batch to be copied stands: tiles, first group, columns of it that are past
+    int f_left = u1 - u0, f_batch = first_batch, f_tile = first_tile, f_stage = 0;
+    int f_kt = kt0 + f_batch * kBatch;
+    int f_grp = f_kt * 64 / a.gs, f_past = f_kt * 64 - f_grp * a.gs;
+    const int grp0 = kt0 * 64 / a.gs, past0 = kt0 * 64 - grp0 * a.gs;
+    const uint8_t* f_src = a.packed + ((size_t)f_tile * P.kt + f_kt) * 512 + lane * 16;
+    const uint8_t* f_steps = a.packed + P.code_bytes() + (size_t)f_tile * a.G * 64 + lane * 16;
+    auto fetch = [&]() {
+        if (f_left > 0) {
+            --f_left;
+            const uint32_t dst = ring32 + f_stage * stage_bytes;
+            if (f_kt + kBatch <= kt1) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (rt < P.mt && kt + u < kt1) {
-                w[u] = load_tile(tiles + ((size_t)rt * P.kt + kt + u) * 32);
-#pragma unroll
-                for (int f = 0; f < kFlush; ++f) {
-                    // a tile's second half may lie behind the last step
-                    const int grp = min((int)((unsigned)((kt + u) * 64 + 32 * f) / (unsigned)a.gs),
-                                        a.G - 1);
-                    s[u][f] = __ldg(steps + ((size_t)rt * a.G + grp) * 8);
-                }
+                for (int u = 0; u < kBatch; ++u) copy16(dst + u * 512, f_src + u * 512);
             } else {
-                w[u] = make_uint4(0, 0, 0, 0);
+                // tiles behind the slice are zeros, which meet zeros of x
 #pragma unroll
-                for (int f = 0; f < kFlush; ++f) s[u][f] = make_float2(0.f, 0.f);
+                for (int u = 0; u < kBatch; ++u)
+                    copy16_or_zero(dst + u * 512, f_src + u * 512, f_kt + u < kt1);
+            }
+            if (lane < 4 * a.batch_groups)
+                copy16_or_zero(dst + kBatch * 512, f_steps + (size_t)f_grp * 64,
+                               f_grp + lane / 4 < a.G);
+            if (STEPS == kAnywhere && lane + 32 < 4 * a.batch_groups)
+                copy16_or_zero(dst + kBatch * 512 + 512, f_steps + (size_t)f_grp * 64 + 512,
+                               f_grp + 8 + lane / 4 < a.G);
+            f_src += kBatch * 512, f_kt += kBatch;
+            f_grp += a.batch_gq, f_past += a.batch_gr;
+            if (f_past >= a.gs) f_past -= a.gs, ++f_grp;
+            if (++f_batch == batches) {
+                f_batch = 0, ++f_tile, f_kt = kt0, f_grp = grp0, f_past = past0;
+                f_src += ((int64_t)P.kt - (int64_t)batches * kBatch) * 512;
+                f_steps += (size_t)a.G * 64;
             }
         }
+        copy_commit();
+        f_stage = f_stage + 1 == kStages ? 0 : f_stage + 1;
     };
-    fetch(rt_first, kt0, cur, scur);
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch();
 
-    const int chunks = max(0, kt1 - kt0) * 8;
-    if constexpr (K == kF32 || K == kF32Book) {
-        stage_x<K, float>(sx, a, t0, count, kt0 * 64, chunks);
-    } else if constexpr (K == kF16) {
-        stage_x<K, __half>(sx, a, t0, count, kt0 * 64, chunks);
-    } else if constexpr (K == kI8) {
-        stage_x<K, int8_t>(sx, a, t0, count, kt0 * 64, chunks);
-    } else if constexpr (K == kF16Book) {
-        if (a.x_dtype == BAKRON_I8) stage_x<K, int8_t>(sx, a, t0, count, kt0 * 64, chunks);
-        else stage_x<K, __half>(sx, a, t0, count, kt0 * 64, chunks);
-    } else {
-        stage_x<K, __nv_bfloat16>(sx, a, t0, count, kt0 * 64, chunks);
-    }
     if constexpr (is_book(K)) {
         // entry e of a plane: codes e % 16 and e / 16, once for every lane
         uint4* dst = reinterpret_cast<uint4*>(const_cast<uint32_t*>(table));
@@ -281,28 +360,40 @@ __global__ void __launch_bounds__(kThreads, 2) matvec4_kernel(const __grid_const
             dst[e] = make_uint4(v, v, v, v);
         }
     }
+    const int xgn = a.Gx > 1 ? (kt1 * 64 + a.gx - 1) / a.gx - xg0 : 0;   // steps of x in the slice
     if constexpr (K == kI8 || K == kF16Book) {
-        if (a.Gx > 1) {
-            const int xgn = (kt1 * 64 + a.gx - 1) / a.gx - xg0;     // groups of the slice
-            for (int e = threadIdx.x; e < kTok * xgn; e += kThreads) {
-                const int tk = e / xgn, q = e - tk * xgn;
-                sxs[e] = tk < count && xg0 + q < a.Gx
-                             ? a.xs[(size_t)(t0 + tk) * a.Gx + xg0 + q] : 0.f;
-            }
+        for (int e = threadIdx.x; e < kTok * xgn; e += kThreads) {
+            const int tk = e / xgn, q = e - tk * xgn;
+            sxs[e] = tk < count && xg0 + q < a.Gx ? a.xs[(size_t)(t0 + tk) * a.Gx + xg0 + q] : 0.f;
         }
     }
+    if (units == 0)                 // a slice behind the last column
+        for (int e = threadIdx.x; e < kTok * rows; e += kThreads) part[e] = 0.f;
+    if (lane == 0) head_tile[warp] = u0 < u1 && first_batch > 0 ? first_tile - rt0 : -1;
+    copy_wait<kStages - 1>();       // x is there; the ring's stages may still be on their way
     __syncthreads();
-    const int xgn = a.Gx > 1 ? (kt1 * 64 + a.gx - 1) / a.gx - xg0 : 0;
+    if constexpr (K == kI8) {
+        // bytes in the order of the masked nibbles: columns 0, 2, 1, 3
+        const int words = batches * kBatch * 4;
+        for (int tk = 0; tk < count; ++tk)
+            for (int e = threadIdx.x; e < words; e += kThreads) {
+                uint4* p = reinterpret_cast<uint4*>(sx + tk * a.pitch) + e;
+                const uint4 v = *p;
+                *p = make_uint4(__byte_perm(v.x, 0, 0x3120), __byte_perm(v.y, 0, 0x3120),
+                                __byte_perm(v.z, 0, 0x3120), __byte_perm(v.w, 0, 0x3120));
+            }
+        __syncthreads();
+    }
 
-    // staged row of this lane's column in each product tile; columns without one multiply zeros
+    // staged row of this lane's column in each product tile. A column without a token takes the
+    // first one: columns do not meet in a product, and nobody reads its sums.
     const char* brow[NT];
-    bool bon[NT];
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
         const int tok = is_split(K) ? 2 * q + (g & 1) : 8 * q + g;
         const int row = is_split(K) ? tok * 3 + g / 2 : tok;
-        bon[q] = tok < count && !(is_split(K) && g >= 6);
-        brow[q] = sx + row * a.pitch + (K == kI8 ? 16 * t : 16 * t);
+        const bool on = tok < count && !(is_split(K) && g >= 6);
+        brow[q] = sx + (on ? row * a.pitch : 0) + (K == kI8 ? 8 : 16) * t;
     }
 
     float tot[NT][4];
@@ -311,142 +402,161 @@ __global__ void __launch_bounds__(kThreads, 2) matvec4_kernel(const __grid_const
 #pragma unroll
         for (int c = 0; c < 4; ++c) tot[q][c] = 0.f;
 
-    const int batches = (max(0, kt1 - kt0) + kAhead - 1) / kAhead;
-    for (int i = 0; i < a.tpw; ++i) {
-        const int rt = rt_first + i * kWarps;
-        for (int b = 0; b < batches; ++b) {
-            const int kt = kt0 + b * kAhead;
-            if (b + 1 < batches) fetch(rt, kt + kAhead, nxt, snxt);
-            else if (i + 1 < a.tpw) fetch(rt + kWarps, kt0, nxt, snxt);
+    int c_stage = 0, c_tile = first_tile, c_batch = first_batch;
+    int past = (kt0 + first_batch * kBatch) * 64 % a.gs;     // columns into the group
+    bool whole = first_batch == 0;      // whether this warp began the tile
+    for (int unit = u0; unit < u1; ++unit) {
+        copy_wait<kStages - 2>();
+        __syncwarp();            // the steps were copied by other lanes; all are done with the
+        fetch();                 // stage before this one, which is filled now
+        const char* stage = ring + c_stage * stage_bytes;
+        c_stage = c_stage + 1 == kStages ? 0 : c_stage + 1;
+        const float2* steps = reinterpret_cast<const float2*>(stage + kBatch * 512) + g;
+        const int xbatch = c_batch * kBatch * 64;
+        const char* xb[NT];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                if (kt + u >= kt1) break;
-                const uint32_t w[4] = {cur[u].x, cur[u].y, cur[u].z, cur[u].w};
-                float d[NT][4];
-                int di[NT][4];
-                uint4 bi[NT];      // int8: both halves at once
+        for (int q = 0; q < NT; ++q) xb[q] = brow[q] + xbatch * (K == kI8 ? 1 : 2);
+        float2 s;
+        if (STEPS == kPerBatch) s = *steps;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const uint4 wv = *reinterpret_cast<const uint4*>(stage + u * 512 + lane * 16);
+            const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w};
+            float d[NT][4];
+            int di[NT][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool fresh = h == 0 || HALF;       // the first products of a sum
+                float z[4] = {0.f, 0.f, 0.f, 0.f};
+                int zi[4] = {0, 0, 0, 0};
+                const uint32_t w0 = w[2 * h], w1 = w[2 * h + 1];
                 if constexpr (K == kI8) {
+                    const uint32_t A[4] = {(w0 << 4) & 0xF0F0F0F0u, (w1 << 4) & 0xF0F0F0F0u,
+                                           w0 & 0xF0F0F0F0u, w1 & 0xF0F0F0F0u};
 #pragma unroll
-                    for (int q = 0; q < NT; ++q)
-                        bi[q] = bon[q] ? *reinterpret_cast<const uint4*>(brow[q] + (kt + u - kt0) * 64)
-                                       : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 0 || HALF) {
-#pragma unroll
-                        for (int q = 0; q < NT; ++q)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) d[q][c] = 0.f, di[q][c] = 0;
+                    for (int q = 0; q < NT; ++q) {
+                        const uint2 B = *reinterpret_cast<const uint2*>(xb[q] + 64 * u + 32 * h);
+                        mma_s8(di[q], A, B.x, B.y, fresh ? zi : di[q]);
                     }
-                    if constexpr (K == kI8) {
-                        const uint32_t A[4] = {(w[2 * h] << 4) & 0xF0F0F0F0u,
-                                               (w[2 * h + 1] << 4) & 0xF0F0F0F0u,
-                                               w[2 * h] & 0xF0F0F0F0u, w[2 * h + 1] & 0xF0F0F0F0u};
+                } else {
+                    uint4 B[NT];      // B0, B1 of the first product, then of the second
 #pragma unroll
-                        for (int q = 0; q < NT; ++q)
-                            mma_s8(di[q], A, h ? bi[q].z : bi[q].x, h ? bi[q].w : bi[q].y);
-                    } else {
-                        uint4 B[NT];
+                    for (int q = 0; q < NT; ++q) {
+                        const uint4 v =
+                            *reinterpret_cast<const uint4*>(xb[q] + 128 * u + 64 * h);
+                        if constexpr (is_book(K))     // pairs as the table gives them
+                            B[q] = make_uint4(__byte_perm(v.x, v.z, 0x5410),
+                                              __byte_perm(v.y, v.w, 0x5410),
+                                              __byte_perm(v.x, v.z, 0x7632),
+                                              __byte_perm(v.y, v.w, 0x7632));
+                        else
+                            B[q] = v;
+                    }
 #pragma unroll
-                        for (int q = 0; q < NT; ++q)
-                            B[q] = bon[q] ? *reinterpret_cast<const uint4*>(
-                                                brow[q] + (kt + u - kt0) * 128 + 64 * h)
-                                          : make_uint4(0, 0, 0, 0);
+                    for (int pl = 0; pl < (is_book(K) ? planes(K) : 1); ++pl) {
+                        uint32_t p0[4], p1[4];
+                        if constexpr (is_book(K)) {
+                            const char* tb = reinterpret_cast<const char*>(table) + pl * 32768;
 #pragma unroll
-                        for (int pl = 0; pl < (is_book(K) ? planes(K) : 1); ++pl) {
-                            uint32_t p0[4], p1[4];
-                            if constexpr (is_book(K)) {
-                                const char* tb = reinterpret_cast<const char*>(table) + pl * 32768;
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const uint32_t u0 = w[2 * h], u1 = w[2 * h + 1];
-                                    const uint32_t s0 = q == 0 ? u0 << 7 : u0 >> (8 * q - 7);
-                                    const uint32_t s1 = q == 0 ? u1 << 7 : u1 >> (8 * q - 7);
-                                    p0[q] = *reinterpret_cast<const uint32_t*>(
-                                        tb + ((s0 & 0x7F80u) | (4 * lane)));
-                                    p1[q] = *reinterpret_cast<const uint32_t*>(
-                                        tb + ((s1 & 0x7F80u) | (4 * lane)));
-                                }
-                            } else if constexpr (is_half(K)) {
-                                codes_f16(w[2 * h], p0);
-                                codes_f16(w[2 * h + 1], p1);
-                            } else {
-                                codes_bf16(w[2 * h], p0);
-                                codes_bf16(w[2 * h + 1], p1);
+                            for (int q = 0; q < 4; ++q) {
+                                const uint32_t s0 = q == 0 ? w0 << 7 : w0 >> (8 * q - 7);
+                                const uint32_t s1 = q == 0 ? w1 << 7 : w1 >> (8 * q - 7);
+                                p0[q] = *reinterpret_cast<const uint32_t*>(
+                                    tb + ((s0 & 0x7F80u) | (4 * lane)));
+                                p1[q] = *reinterpret_cast<const uint32_t*>(
+                                    tb + ((s1 & 0x7F80u) | (4 * lane)));
                             }
-                            const uint32_t A0[4] = {p0[0], p1[0], p0[1], p1[1]};
-                            const uint32_t A1[4] = {p0[2], p1[2], p0[3], p1[3]};
-#pragma unroll
-                            for (int q = 0; q < NT; ++q) {
-                                if constexpr (is_half(K)) {
-                                    mma_f16(d[q], A0, B[q].x, B[q].y);
-                                    mma_f16(d[q], A1, B[q].z, B[q].w);
-                                } else {
-                                    mma_bf16(d[q], A0, B[q].x, B[q].y);
-                                    mma_bf16(d[q], A1, B[q].z, B[q].w);
-                                }
-                            }
+                        } else if constexpr (is_half(K)) {
+                            codes_f16(w0, p0);
+                            codes_f16(w1, p1);
+                        } else {
+                            codes_bf16(w0, p0);
+                            codes_bf16(w1, p1);
                         }
-                    }
-                    if (h == 1 || HALF) {
-                        const float2 s = scur[u][HALF ? h : 0];
+                        const uint32_t A0[4] = {p0[0], p1[0], p0[1], p1[1]};
+                        const uint32_t A1[4] = {p0[2], p1[2], p0[3], p1[3]};
 #pragma unroll
                         for (int q = 0; q < NT; ++q) {
-                            float s4[4] = {s.x, s.x, s.y, s.y};
-                            if constexpr (K == kI8 || K == kF16Book) {
-                                if (a.Gx > 1) {
-                                    const int xg = ((kt + u) * 64 + (HALF ? 32 * h : 0)) / a.gx - xg0;
-                                    const float* xr = sxs + (8 * q + 2 * t) * xgn + min(xg, xgn - 1);
-                                    const float x0 = xr[0], x1 = xr[xgn];
-                                    s4[0] *= x0, s4[1] *= x1, s4[2] *= x0, s4[3] *= x1;
-                                }
+                            if constexpr (is_half(K)) {
+                                mma_f16(d[q], A0, B[q].x, B[q].y, fresh && pl == 0 ? z : d[q]);
+                                mma_f16(d[q], A1, B[q].z, B[q].w, d[q]);
+                            } else {
+                                mma_bf16(d[q], A0, B[q].x, B[q].y, fresh && pl == 0 ? z : d[q]);
+                                mma_bf16(d[q], A1, B[q].z, B[q].w, d[q]);
                             }
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                tot[q][c] = fmaf(s4[c], K == kI8 ? (float)di[q][c] : d[q][c],
-                                                 tot[q][c]);
                         }
                     }
                 }
-            }
+                if (h == 1 || HALF) {
+                    if constexpr (STEPS == kPerTile) s = steps[(u >> a.step_shift) * 8];
+                    if constexpr (STEPS == kAnywhere) {
+                        s = *steps;
+                        past += 32;
+                        if (past >= a.gs) past -= a.gs, steps += 8;
+                    }
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                cur[u] = nxt[u];
+                    for (int q = 0; q < NT; ++q) {
+                        float s4[4] = {s.x, s.x, s.y, s.y};
+                        if constexpr (K == kI8 || K == kF16Book) {
+                            if (a.Gx > 1) {
+                                const int xg = (kt0 * 64 + xbatch + 64 * u + (HALF ? 32 * h : 0)) / a.gx - xg0;
+                                const float* xr = sxs + (8 * q + 2 * t) * xgn + min(xg, xgn - 1);
+                                const float x0 = xr[0], x1 = xr[xgn];
+                                s4[0] *= x0, s4[1] *= x1, s4[2] *= x0, s4[3] *= x1;
+                            }
+                        }
 #pragma unroll
-                for (int f = 0; f < kFlush; ++f) scur[u][f] = snxt[u][f];
-            }
-        }
-        // this row tile's sums to shared memory
-        const int r0 = (warp + i * kWarps) * 16 + g;
-#pragma unroll
-        for (int q = 0; q < NT; ++q) {
-            if constexpr (is_split(K)) {      // columns 0..5: part (lane t) of tokens 2 q, 2 q + 1
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float v = tot[q][c];
-                    v += __shfl_xor_sync(0xffffffffu, v, 2);
-                    v += __shfl_xor_sync(0xffffffffu, v, 1);
-                    if (t == 0) part[(2 * q + (c & 1)) * rows + r0 + 8 * (c >> 1)] = v;
+                        for (int c = 0; c < 4; ++c)
+                            tot[q][c] = fmaf(s4[c], K == kI8 ? (float)di[q][c] : d[q][c],
+                                             tot[q][c]);
+                    }
                 }
-            } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    part[(8 * q + 2 * t + (c & 1)) * rows + r0 + 8 * (c >> 1)] = tot[q][c];
             }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tot[q][c] = 0.f;
         }
+        if (++c_batch == batches || unit + 1 == u1) {
+            // the tile's sums: whole tiles and a tile's first part to its rows, the end of a tile
+            // that another warp began to this warp's place
+            float* out = whole ? part + (c_tile - rt0) * 16 : head + warp * kTok * 16;
+            const int ld = whole ? rows : 16;
+#pragma unroll
+            for (int q = 0; q < NT; ++q) {
+                if constexpr (is_split(K)) {  // columns 0..5: part (lane t) of tokens 2 q, 2 q + 1
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float v = t == 3 ? 0.f : tot[q][c];
+                        v += __shfl_xor_sync(0xffffffffu, v, 2);
+                        v += __shfl_xor_sync(0xffffffffu, v, 1);
+                        if (t == 0) out[(2 * q + (c & 1)) * ld + g + 8 * (c >> 1)] = v;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        out[(8 * q + 2 * t + (c & 1)) * ld + g + 8 * (c >> 1)] = tot[q][c];
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tot[q][c] = 0.f;
+            }
+            c_batch = 0, ++c_tile, past = past0;
+            whole = true;
+        }
+    }
+    __syncthreads();
+    // ends of tiles that another warp began, warp after warp (one thread an element)
+    for (int w = 1; w < kWarps; ++w) {
+        const int tile = head_tile[w];
+        if (tile < 0) continue;
+        for (int e = threadIdx.x; e < kTok * 16; e += kThreads)
+            part[(e / 16) * rows + tile * 16 + e % 16] += head[w * kTok * 16 + e];
     }
 
     // the blocks of the cluster add up a share of the rows each
     if (ck > 1) cluster.sync();
     else __syncthreads();
-    const int share = rows / ck;
+    const int mine = (rt1 - rt0) * 16, share = (mine + ck - 1) / ck;
     for (int e = threadIdx.x; e < share * count; e += kThreads) {
         const int tk = e / share, r = rank * share + e - tk * share;
-        const int64_t i = (int64_t)block * rows + r;
-        if (i >= a.m) continue;
+        const int64_t i = (int64_t)rt0 * 16 + r;
+        if (r >= mine || i >= a.m) continue;
         float v = 0.f;
         for (int c = 0; c < ck; ++c)
             v += (ck > 1 ? cluster.map_shared_rank(part, c) : part)[tk * rows + r];
@@ -462,18 +572,16 @@ __global__ void __launch_bounds__(kThreads, 2) matvec4_kernel(const __grid_const
 }
 
 // ------------------------------------------------------------------------------------- host
-template <int K, int NT, bool HALF>
+template <int K, int NT, int STEPS>
 int launch(const Args& a, int ck, size_t smem, cudaStream_t st) {
-    auto kern = matvec4_kernel<K, NT, HALF>;
+    auto kern = matvec4_kernel<K, NT, STEPS>;
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
             cudaSuccess)
         return BAKRON_ERR_CUDA;
-    const int rows = kWarps * a.tpw * 16, tok = NT * tile_tokens(K);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.m + (long long)rows - 1) / rows * ck),
-                       (unsigned)((a.tokens + tok - 1) / tok));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)(a.clusters * ck), (unsigned)((a.tokens + a.chunk - 1) / a.chunk));
+    cfg.blockDim = dim3(warps_of(K) * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -487,39 +595,100 @@ int launch(const Args& a, int ck, size_t smem, cudaStream_t st) {
     return cuda_err(e);
 }
 
+// One way to cut the work: ck slices of the columns, the row tiles dealt out over clusters of ck
+// blocks, as many as fit the GPU at once (times the chunks of tokens).
+struct Cut { int ck = 0, slice, pitch, chunk, clusters, max_tiles; size_t smem; double cost; };
+
 template <int K>
-int plan(Args& a, cudaStream_t st) {
+Cut cut(const Args& a, int ck, int nt, int sms) {
     const Pack4Shape P(a.m, a.n, a.G);
-    const int blocks = (P.mt + kWarps - 1) / kWarps;
-    // Slices of the columns: as many as keep four tiles a warp, until there are 4 blocks an SM.
-    int ck = 1;
-    while (ck < 8 && P.kt >= 8 * ck && blocks * ck < 4 * 148) ck *= 2;
-    // or as many as bring the staged activations of one product tile into shared memory
-    while (ck < 8 && (P.kt + ck - 1) / ck > 64) ck *= 2;
-    a.slice = (P.kt + ck - 1) / ck;
-    a.tpw = 1;
-    const int row_bytes = a.slice * 64 * (K == kI8 ? 1 : 2);
-    a.pitch = row_bytes % 128 ? row_bytes : row_bytes + 64;    // odd multiple of 64: no conflicts
-    const int rows = kWarps * a.tpw * 16;
-    const auto bytes = [&](int nt) {
-        const size_t tok = (size_t)nt * tile_tokens(K);
-        size_t b = tok * token_rows(K) * a.pitch + tok * rows * 4;
+    constexpr int kBatch = batch_of(K);
+    Cut c;
+    c.slice = (P.kt + ck - 1) / ck;
+    c.slice = (c.slice + kBatch - 1) / kBatch * kBatch;
+    // rows of staged activations, apart by what keeps their reads free of bank conflicts
+    const int row = c.slice * 64 * (K == kI8 ? 1 : 2);
+    c.pitch = K == kI8 ? row + 32 : row % 128 ? row : row + 64;
+    const int tok = nt * tile_tokens(K);
+    const size_t limit = 227 * 1024;
+    const auto bytes = [&] {
+        size_t b = (size_t)warps_of(K) * kStages * (kBatch * 512 + a.batch_groups * 64) +
+                   (size_t)c.chunk * token_rows(K) * c.pitch +
+                   (size_t)tok * 16 * 4 * (c.max_tiles + warps_of(K));
         if (is_book(K)) b += planes(K) * 32768;
-        if (a.Gx > 1) b += tok * 4 * ((size_t)a.slice * 64 / a.gx + 2);
+        if (a.Gx > 1) b += (size_t)tok * 4 * ((size_t)c.slice * 64 / a.gx + 2);
         return b;
     };
-    int nt = a.tokens <= tile_tokens(K) ? 1 : a.tokens <= 2 * tile_tokens(K) ? 2 : 4;
-    while (nt > 1 && bytes(nt) > 110 * 1024) nt /= 2;
-    const size_t smem = bytes(nt);
-    if (smem > 227 * 1024) return BAKRON_ERR_INVALID_ARG;
-    const bool half = (a.G > 1 && a.gs % 64) || (a.Gx > 1 && a.gx % 64);
-    if (half)
-        return nt == 1 ? launch<K, 1, true>(a, ck, smem, st)
-             : nt == 2 ? launch<K, 2, true>(a, ck, smem, st)
-                       : launch<K, 4, true>(a, ck, smem, st);
-    return nt == 1 ? launch<K, 1, false>(a, ck, smem, st)
-         : nt == 2 ? launch<K, 2, false>(a, ck, smem, st)
-                   : launch<K, 4, false>(a, ck, smem, st);
+    c.chunk = std::min(a.tokens, tok);
+    // SMs that clusters of ck blocks can fill (they do not cross a GPC): 132 of 148 in fours, 120 in
+    // eights, as the occupancy query says; one more would wait for a second wave
+    const int fit = ck <= 2 ? sms : ck == 4 ? sms * 33 / 37 : sms * 30 / 37;
+    // blocks an SM and row tiles a cluster depend on each other through shared memory: from the
+    // most blocks down to what fits
+    for (int occ = blocks_of(K); occ >= 1; --occ) {
+        for (;; c.chunk /= 2) {
+            const int chunks = (a.tokens + c.chunk - 1) / c.chunk;
+            c.clusters = std::max(1, std::min(P.mt, occ * fit / ck / std::min(chunks, 1 << 20)));
+            c.max_tiles = (P.mt + c.clusters - 1) / c.clusters;
+            // sums of at most 64 row tiles stay in shared memory: more clusters than fit at once
+            if (c.max_tiles > 64) c.max_tiles = 64, c.clusters = (P.mt + 63) / 64;
+            c.smem = bytes();
+            if (occ * (c.smem + 1024) <= 228 * 1024 && c.smem <= limit) {
+                // tiles an SM goes through, and its share of staged activations (from L2)
+                const long long per_sm = ((long long)c.clusters * ck * chunks + sms - 1) / sms;
+                c.ck = ck;
+                c.cost = (double)per_sm * (c.max_tiles * (double)c.slice +
+                                           0.08 * c.slice * c.chunk * token_rows(K) + 4.0);
+                return c;
+            }
+            if (occ > 1 || c.chunk == 1) break;
+        }
+    }
+    return c;
+}
+
+template <int K>
+int plan(Args& a, cudaStream_t st) {
+    const int sms = tc::sm_count();
+    if (sms <= 0) return BAKRON_ERR_CUDA;
+    const Pack4Shape P(a.m, a.n, a.G);
+    constexpr int kBatch = batch_of(K), cols = kBatch * 64;
+    a.batch_groups = a.G == 1 || a.gs % cols == 0 ? 1
+                     : cols % a.gs == 0           ? cols / a.gs
+                                                  : (cols - 1) / a.gs + 2;
+    a.batch_gq = cols / a.gs, a.batch_gr = cols % a.gs;
+    Cut best;
+    int best_nt = 1;
+    for (int nt = 1; nt <= 4; nt *= 2) {
+        if (nt > 1 && a.tokens <= nt / 2 * tile_tokens(K)) break;
+        for (int ck = 1; ck <= 8 && (ck == 1 || P.kt >= kBatch * ck); ck *= 2) {
+            const Cut c = cut<K>(a, ck, nt, sms);
+            if (c.ck && (!best.ck || c.cost < best.cost)) best = c, best_nt = nt;
+        }
+    }
+    if (!best.ck) return BAKRON_ERR_INVALID_ARG;
+    a.slice = best.slice, a.pitch = best.pitch, a.chunk = best.chunk;
+    a.clusters = best.clusters, a.max_tiles = best.max_tiles;
+    a.tiles_each = P.mt / a.clusters, a.tiles_rest = P.mt % a.clusters;
+    const int ck = best.ck;
+    const size_t smem = best.smem;
+    // batches begin at multiples of `cols` columns
+    a.step_shift = a.gs == 64 ? 0 : a.gs == 128 ? 1 : 2;
+    int steps = a.G == 1 || a.gs % cols == 0                    ? kPerBatch
+                : a.gs >= 64 && cols % a.gs == 0 ? kPerTile
+                                                 : kAnywhere;
+    if (a.Gx > 1 && a.gx % 64) steps = kAnywhere;
+    switch (best_nt * 4 + steps) {
+        case 4: return launch<K, 1, kPerBatch>(a, ck, smem, st);
+        case 5: return launch<K, 1, kPerTile>(a, ck, smem, st);
+        case 6: return launch<K, 1, kAnywhere>(a, ck, smem, st);
+        case 8: return launch<K, 2, kPerBatch>(a, ck, smem, st);
+        case 9: return launch<K, 2, kPerTile>(a, ck, smem, st);
+        case 10: return launch<K, 2, kAnywhere>(a, ck, smem, st);
+        case 16: return launch<K, 4, kPerBatch>(a, ck, smem, st);
+        case 17: return launch<K, 4, kPerTile>(a, ck, smem, st);
+        default: return launch<K, 4, kAnywhere>(a, ck, smem, st);
+    }
 }
 
 uint32_t bits_of(float f) {
@@ -596,7 +765,7 @@ extern "C" int bakron_matvec4(const void* packed, int m, int n, int group_size,
     a.packed = static_cast<const uint8_t*>(packed);
     a.m = m, a.n = n;
     a.G = group_count(group_size, n);
-    a.gs = a.G > 1 ? group_size : 64 * ((n + 63) / 64);
+    a.gs = a.G > 1 ? group_size : 1 << 30;     // one step: no column is past it
     a.x = x, a.x_dtype = x_dtype, a.ldx = ldx, a.xs = x_scales;
     a.Gx = i8 ? group_count(x_group_size, n) : 1;
     a.gx = a.Gx > 1 ? x_group_size : 64 * ((n + 63) / 64);
