@@ -3,19 +3,39 @@
 //   q = softmax(z / tau),  p_j = exp(t_j / tau - T),
 //   loss = w sum_j p_j (log p_j - log q_{i_j}),   dz_i = (w / tau) (M q_i - sum_{j: i_j = i} p_j)
 //
-// One block per row: one pass with the running maximum and sum of each thread, the block's total,
-// then the gradient from a second look at the row. All statistics are fp32.
+// Bound by bytes: a row of the vocabulary read once, and written once with the gradient. A row is
+// shared by a cluster of 1 to 8 blocks, each of which keeps its slice in registers (128 bytes a
+// thread, 64 KB a block, two blocks an SM): all loads of a slice are in flight at once, the maximum
+// and the sum come from one look at it, and the gradient needs no second read. The blocks exchange
+// (maximum, sum) pairs of their warps through distributed shared memory, one barrier a row, and join
+// them in a fixed order. Rows above 512 KB are streamed twice instead (the second time from L2). Few
+// rows are cut finer, so that they fill the GPU.
+//
+// All statistics are fp32. Differences from a maximum are taken before they are scaled by 1 / tau, so
+// that nothing large cancels in log p - log q; exponentials are ex2.approx (2 units in the last place).
+#include <cooperative_groups.h>
+
 #include <cmath>
 
 #include "lowp.cuh"
+#include "tcgemm_host.cuh"
 
 namespace bakron {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
 constexpr int kMaxK = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -INFINITY;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // Joins the pairs (m, s) and (m2, s2) that stand for s 2^(c m) and s2 2^(c m2).
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float c) {
@@ -24,7 +44,7 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2, flo
         s += s2;
         return;
     }
-    s = s * exp2f((m - top) * c) + s2 * exp2f((m2 - top) * c);
+    s = s * ex2((m - top) * c) + s2 * ex2((m2 - top) * c);
     m = top;
 }
 
@@ -42,7 +62,7 @@ __device__ __forceinline__ float logit_at(const Teacher& T, size_t e) {
     return to_f32(static_cast<const __nv_bfloat16*>(T.t)[e]);
 }
 
-// Sum over the block in a fixed order; every thread gets it.
+// Sum and maximum over the block in a fixed order; every thread gets them.
 __device__ __forceinline__ float block_sum(float v, float* red) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -50,7 +70,8 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x / 32] = v;
     __syncthreads();
     float s = 0.f;
-    for (int k = 0; k < kThreads / 32; ++k) s += red[k];
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) s += red[k];
     return s;
 }
 __device__ __forceinline__ float block_max(float v, float* red) {
@@ -60,110 +81,360 @@ __device__ __forceinline__ float block_max(float v, float* red) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x / 32] = v;
     __syncthreads();
     float s = kNegInf;
-    for (int k = 0; k < kThreads / 32; ++k) s = fmaxf(s, red[k]);
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) s = fmaxf(s, red[k]);
     return s;
 }
 
-template <class X>
-__global__ void __launch_bounds__(kThreads)
-distill_kernel(const X* z, int V, int64_t ld, Teacher T, float* __restrict__ loss,
+// The elements of 16 bytes as fp32 and back, and the larger ones of two vectors (NaN loses).
+template <class X> struct Vec;
+template <> struct Vec<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void get(const uint4& v, float (&f)[4]) {
+        f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
+        f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ uint4 put(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                          __float_as_uint(f[3]));
+    }
+    static __device__ __forceinline__ uint4 top(const uint4& a, const uint4& b) {
+        const auto f = [](uint32_t x, uint32_t y) {
+            return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y)));
+        };
+        return make_uint4(f(a.x, b.x), f(a.y, b.y), f(a.z, b.z), f(a.w, b.w));
+    }
+    static __device__ __forceinline__ uint4 fill_low() {
+        return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+    }
+};
+template <> struct Vec<__half> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void get(const uint4& v, float (&f)[8]) {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
+            f[2 * k] = p.x, f[2 * k + 1] = p.y;
+        }
+    }
+    static __device__ __forceinline__ uint4 put(const float (&f)[8]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __half2 p = __floats2half2_rn(f[2 * k], f[2 * k + 1]);
+            u[k] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    static __device__ __forceinline__ uint4 top(const uint4& a, const uint4& b) {
+        const auto f = [](uint32_t x, uint32_t y) {
+            const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&x),
+                                      *reinterpret_cast<const __half2*>(&y));
+            return *reinterpret_cast<const uint32_t*>(&m);
+        };
+        return make_uint4(f(a.x, b.x), f(a.y, b.y), f(a.z, b.z), f(a.w, b.w));
+    }
+    static __device__ __forceinline__ uint4 fill_low() {
+        return make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u);
+    }
+};
+template <> struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void get(const uint4& v, float (&f)[8]) {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f[2 * k] = __uint_as_float(u[k] << 16);
+            f[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 put(const float (&f)[8]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+            u[k] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    static __device__ __forceinline__ uint4 top(const uint4& a, const uint4& b) {
+        const auto f = [](uint32_t x, uint32_t y) {
+            const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&x),
+                                      *reinterpret_cast<const __nv_bfloat162*>(&y));
+            return *reinterpret_cast<const uint32_t*>(&m);
+        };
+        return make_uint4(f(a.x, b.x), f(a.y, b.y), f(a.z, b.z), f(a.w, b.w));
+    }
+    static __device__ __forceinline__ uint4 fill_low() {
+        return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+    }
+};
+
+// NV: 16-byte vectors that a thread holds (LOOP: of one round of the stream).
+template <class X, int NV, bool LOOP>
+__global__ void __launch_bounds__(kThreads, 2)
+distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict__ loss,
                float* __restrict__ lse, X* dz, int64_t ldd, int* __restrict__ status) {
-    __shared__ float red[2][kThreads / 32];
-    __shared__ float p[kMaxK], zt[kMaxK];
-    __shared__ int at[kMaxK];
-    const int row = blockIdx.x, tid = threadIdx.x;
+    constexpr int N = Vec<X>::N;
+    __shared__ float red[kWarps];
+    __shared__ float2 pairs[8 * kWarps];              // (maximum, sum) of the cluster's warps
+    __shared__ float p[kMaxK], lp[kMaxK], zt[kMaxK];
+    __shared__ __align__(16) int at[kMaxK];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ck = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int row = blockIdx.x / ck, tid = threadIdx.x;
     const float w = T.w ? T.w[row] : 1.f;
     z += (int64_t)row * ld;
     if (dz) dz += (int64_t)row * ldd;
+
+    // The row: `head` elements up to a 16-byte boundary, `body` vectors, the rest. The blocks
+    // share the vectors; head and rest (16 elements at most) are the first block's, one a thread.
+    const int head = min(V, (int)((16 - reinterpret_cast<uintptr_t>(z) % 16) % 16 / sizeof(X)));
+    const int body = (V - head) / N, rest = V - head - body * N;
+    const int v0 = (int)((long long)body * rank / ck), v1 = (int)((long long)body * (rank + 1) / ck);
+    int extra = -1;
+    if (rank == 0) extra = tid < head ? tid : tid >= 32 && tid < 32 + rest ? V - rest + tid - 32 : -1;
+    const uint4* zv = reinterpret_cast<const uint4*>(z + head);
+    // the gradient's row may lie otherwise to the boundaries: element by element then
+    const bool wide = reinterpret_cast<uintptr_t>(dz + head) % 16 == 0;
+
     if (w == 0.f) {
-        if (tid == 0) loss[row] = 0.f, lse[row] = 0.f;
-        if (dz)
-            for (int i = tid; i < V; i += kThreads) from_f32(0.f, dz[i]);
+        if (rank == 0 && tid == 0) loss[row] = 0.f, lse[row] = 0.f;
+        if (dz) {
+            if (extra >= 0) from_f32(0.f, dz[extra]);
+            for (int i = v0 + tid; i < v1; i += kThreads) {
+                if (wide) {
+                    reinterpret_cast<uint4*>(dz + head)[i] = make_uint4(0, 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < N; ++c) from_f32(0.f, dz[head + (int64_t)i * N + c]);
+                }
+            }
+        }
         return;
     }
-    // the teacher's list; differences from a maximum are taken before they are scaled, so that
-    // nothing large cancels in log p - log q
-    float tmax = kNegInf;
-    for (int j = tid; j < T.k; j += kThreads) {
-        const size_t e = (size_t)row * T.k + j;
-        const long long i = index_at(T, e);
-        const float t = logit_at(T, e);
-        if (i >= V) set_status(status, BAKRON_ERR_INVALID_ARG);
-        const bool there = i >= 0 && i < V && t != kNegInf;
-        at[j] = there ? (int)i : -1;
-        p[j] = t;
-        zt[j] = there ? to_f32(z[i]) : 0.f;
-        if (there) tmax = fmaxf(tmax, t);
+
+    // the slice is on its way before the teacher's list is looked at
+    uint4 v[NV];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const int i = base + u * kThreads + tid;
+            v[u] = i < v1 ? zv[i] : Vec<X>::fill_low();
+        }
+    };
+    load(v0);
+    const float zx = extra >= 0 ? to_f32(z[extra]) : kNegInf;
+    if (ck > 1) cluster.barrier_arrive();        // (every block has begun: see the exchange)
+
+    // the teacher's list: p, log p and the student's logits there; the first block needs them for
+    // the loss, the others for their part of the gradient
+    float mass = 0.f;
+    if (rank == 0 || dz) {
+        float tmax = kNegInf;
+        for (int j = tid; j < T.k; j += kThreads) {
+            const size_t e = (size_t)row * T.k + j;
+            const long long i = index_at(T, e);
+            const float t = logit_at(T, e);
+            if (i >= V) set_status(status, BAKRON_ERR_INVALID_ARG);
+            const bool there = i >= 0 && i < V && t != kNegInf;
+            at[j] = there ? (int)i : -1;
+            lp[j] = t;
+            zt[j] = there ? to_f32(z[i]) : 0.f;
+            if (there) tmax = fmaxf(tmax, t);
+        }
+        if (tid < 3 && T.k + tid < kMaxK) at[T.k + tid] = -1;      // whole int4s
+        float tl = 0.f;      // log p_j = (t_j - tmax) / tau - tl
+        if (T.lse) {
+            tmax = 0.f;
+            tl = T.lse[row];
+        } else {
+            tmax = block_max(tmax, red);
+            float s = 0.f;
+            for (int j = tid; j < T.k; j += kThreads)
+                if (at[j] >= 0) s += expf((lp[j] - tmax) * T.inv_tau);
+            tl = logf(block_sum(s, red));
+        }
+        for (int j = tid; j < T.k; j += kThreads) {
+            float pj = 0.f;
+            if (at[j] >= 0) {
+                lp[j] = (lp[j] - tmax) * T.inv_tau - tl;
+                pj = expf(lp[j]);
+            }
+            p[j] = pj;
+            mass += pj;
+        }
+        mass = block_sum(mass, red);
     }
-    float tl = 0.f;      // log p_j = (t_j - tmax) / tau - tl
-    if (T.lse) {
-        tmax = 0.f;
-        tl = T.lse[row];
-    } else {
-        tmax = block_max(tmax, red[0]);
-        float s = 0.f;
-        for (int j = tid; j < T.k; j += kThreads)
-            if (at[j] >= 0) s += expf((p[j] - tmax) * T.inv_tau);
-        tl = logf(block_sum(s, red[0]));
-    }
-    // the row: its maximum m and s = sum 2^(c (z - m))
+
+    // the slice's maximum and sum of 2^(c (z - maximum)), warp by warp
     const float c = T.inv_tau * kLog2e;
-    float m = kNegInf, s = 0.f;
-    for (int i = tid; i < V; i += kThreads) {
-        const float v = to_f32(z[i]);
-        if (v > m) {
-            s = s * exp2f((m - v) * c) + 1.f;
-            m = v;
-        } else if (v != kNegInf) {
-            s += exp2f((v - m) * c);
+    float m = zx, s = 0.f;
+    auto thread_max = [&] {
+        uint4 b = Vec<X>::fill_low();
+#pragma unroll
+        for (int u = 0; u < NV; ++u) b = Vec<X>::top(b, v[u]);
+        float f[N], a = kNegInf;
+        Vec<X>::get(b, f);
+#pragma unroll
+        for (int k = 0; k < N; ++k) a = fmaxf(a, f[k]);
+        return a;
+    };
+    // a warp whose elements are all -inf (or NaN) counts its differences from 0
+    auto thread_sum = [&](float top) {
+        const float ref = top == kNegInf ? 0.f : top;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            float f[N];
+            Vec<X>::get(v[u], f);
+#pragma unroll
+            for (int k = 0; k < N; ++k) part[k % 4] += ex2((f[k] - ref) * c);
+        }
+        return (part[0] + part[1]) + (part[2] + part[3]);
+    };
+    auto warp_max = [](float a) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        return a;
+    };
+    if constexpr (!LOOP) {
+        m = warp_max(fmaxf(m, thread_max()));
+        s = thread_sum(m);
+        if (extra >= 0) s += ex2((zx - (m == kNegInf ? 0.f : m)) * c);
+    } else {
+        m = warp_max(m);
+        if (extra >= 0) s = ex2((zx - (m == kNegInf ? 0.f : m)) * c);
+        for (int base = v0;;) {
+            const float top = fmaxf(m, warp_max(thread_max()));
+            if (top > m) s = m == kNegInf ? s : s * ex2((m - top) * c), m = top;
+            s += thread_sum(m);
+            base += NV * kThreads;
+            if (base >= v1) break;
+            load(base);
         }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o), c);
-    __syncthreads();
-    if ((tid & 31) == 0) red[0][tid / 32] = m, red[1][tid / 32] = s;
-    __syncthreads();
-    m = red[0][0], s = red[1][0];
-    for (int k = 1; k < kThreads / 32; ++k) join(m, s, red[0][k], red[1][k], c);
-    if (fabsf(m) == INFINITY) s = NAN;      // +inf, or nothing but -inf
-    const float l = logf(s);
-    float kl = 0.f, mass = 0.f;
-    for (int j = tid; j < T.k; j += kThreads) {
-        float pj = 0.f;
-        if (at[j] >= 0) {
-            const float lp = (p[j] - tmax) * T.inv_tau - tl;
-            pj = expf(lp);
-            if (pj != 0.f) kl += pj * (lp - ((zt[j] - m) * T.inv_tau - l));
-        }
-        p[j] = pj;
-        mass += pj;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (ck > 1) {
+        cluster.barrier_wait();
+        if ((tid & 31) < ck)
+            cluster.map_shared_rank(pairs, tid & 31)[rank * kWarps + tid / 32] = make_float2(m, s);
+        cluster.sync();
+    } else {
+        if ((tid & 31) == 0) pairs[tid / 32] = make_float2(m, s);
+        __syncthreads();
     }
-    kl = block_sum(kl, red[0]);
-    mass = block_sum(mass, red[0]);
-    if (tid == 0) loss[row] = w * kl, lse[row] = m * T.inv_tau + l;
+    m = kNegInf, s = 0.f;
+    for (int k = tid & 31; k < ck * kWarps; k += 32) join(m, s, pairs[k].x, pairs[k].y, c);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        // both lanes of a pair join in the same order
+        float m1 = m, s1 = s, m2 = __shfl_xor_sync(0xffffffffu, m, o),
+              s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        if (tid & o) join(m2, s2, m1, s1, c), m = m2, s = s2;
+        else join(m1, s1, m2, s2, c), m = m1, s = s1;
+    }
+    if (fabsf(m) == INFINITY) s = NAN;      // +inf, or nothing but -inf
+    if (rank == 0) {
+        const float l = logf(s);
+        float kl = 0.f;
+        for (int j = tid; j < T.k; j += kThreads)
+            if (p[j] != 0.f) kl += p[j] * (lp[j] - ((zt[j] - m) * T.inv_tau - l));
+        kl = block_sum(kl, red);
+        if (tid == 0) loss[row] = w * kl, lse[row] = m * T.inv_tau + l;
+    }
     if (!dz) return;
+
+    // the gradient: every element, then those of the list once more (from the packed values: the
+    // unpacked ones would take twice the registers all the way)
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+        asm volatile("" : "+r"(v[u].x), "+r"(v[u].y), "+r"(v[u].z), "+r"(v[u].w));
     const float f = w * T.inv_tau;
-    const float fq = mass == 0.f ? 0.f : f * mass / s;
-    for (int i = tid; i < V; i += kThreads)
-        from_f32(mass == 0.f ? 0.f : fq * exp2f((to_f32(z[i]) - m) * c), dz[i]);
+    const bool none = mass == 0.f;
+    const float fq = none ? 0.f : f * mass / s;
+    auto grad = [&](float x) { return none ? 0.f : fq * ex2((x - m) * c); };
+    if (extra >= 0) from_f32(grad(zx), dz[extra]);
+    for (int base = v0; base < v1; base += NV * kThreads) {
+        if (LOOP) load(base);
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const int i = base + u * kThreads + tid;
+            if (i >= v1) break;
+            float x[N];
+            Vec<X>::get(v[u], x);
+#pragma unroll
+            for (int k = 0; k < N; ++k) x[k] = grad(x[k]);
+            if (wide) {
+                reinterpret_cast<uint4*>(dz + head)[i] = Vec<X>::put(x);
+            } else {
+#pragma unroll
+                for (int k = 0; k < N; ++k) from_f32(x[k], dz[head + (int64_t)i * N + k]);
+            }
+        }
+    }
+    if (none) return;
     __syncthreads();
     for (int j = tid; j < T.k; j += kThreads) {
-        if (at[j] < 0 || mass == 0.f) continue;
-        float pj = 0.f;
-        for (int k = 0; k < T.k; ++k) pj += at[k] == at[j] ? p[k] : 0.f;
-        from_f32(fq * exp2f((zt[j] - m) * c) - f * pj, dz[at[j]]);
+        const int i = at[j];
+        if (i < 0) continue;
+        const int vec = i < head || i >= V - rest ? -1 : (i - head) / N;
+        if (vec < 0 ? rank != 0 : vec < v0 || vec >= v1) continue;
+        float pj = 0.f;              // all entries of this index, in the list's order
+        for (int k = 0; k < T.k; k += 4) {
+            const int4 a = *reinterpret_cast<const int4*>(at + k);
+            if (a.x == i) pj += p[k];
+            if (a.y == i) pj += p[k + 1];
+            if (a.z == i) pj += p[k + 2];
+            if (a.w == i) pj += p[k + 3];
+        }
+        from_f32(fq * ex2((zt[j] - m) * c) - f * pj, dz[i]);
     }
 }
 
-template <int D>
-int launch(const void* z, int rows, int V, int64_t ld, const Teacher& T, float* loss, float* lse,
-           void* dz, int64_t ldd, int* status, cudaStream_t st) {
-    using X = typename Elem<D>::T;
-    distill_kernel<X><<<rows, kThreads, 0, st>>>(static_cast<const X*>(z), V, ld, T, loss, lse,
-                                                 static_cast<X*>(dz), ldd, status);
+template <class X, int NV, bool LOOP>
+int launch(const X* z, int rows, int V, int64_t ld, const Teacher& T, float* loss, float* lse, X* dz,
+           int64_t ldd, int* status, int ck, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)rows * ck);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ck;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, distill_kernel<X, NV, LOOP>, z, V, ld, T, loss,
+                                             lse, dz, ldd, status);
     count_launches(1);
-    return cuda_err(cudaGetLastError());
+    return cuda_err(e);
+}
+
+template <int D>
+int plan(const void* z_, int rows, int V, int64_t ld, const Teacher& T, float* loss, float* lse,
+         void* dz_, int64_t ldd, int* status, cudaStream_t st) {
+    using X = typename Elem<D>::T;
+    const X* z = static_cast<const X*>(z_);
+    X* dz = static_cast<X*>(dz_);
+    const int sms = tc::sm_count();
+    if (sms <= 0) return BAKRON_ERR_CUDA;
+    // Blocks a row: as many as keep its slices within 8 vectors a thread, and for few rows as
+    // many as fill the GPU twice, as long as a slice has a vector for every thread.
+    const int vecs = V / Vec<X>::N;
+    int ck = 1;
+    while (ck < 8 && vecs > ck * 8 * kThreads) ck *= 2;
+    while (ck < 8 && (long long)rows * ck * 2 <= 2 * sms && vecs > ck * kThreads) ck *= 2;
+    if ((long long)rows * ck > INT32_MAX) return BAKRON_ERR_INVALID_ARG;
+    const int nv = (vecs + ck * kThreads - 1) / (ck * kThreads);
+    // a slice is ceil(vecs / ck) vectors at most
+    if (nv <= 1) return launch<X, 1, false>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
+    if (nv <= 2) return launch<X, 2, false>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
+    if (nv <= 4) return launch<X, 4, false>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
+    if (nv <= 8) return launch<X, 8, false>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
+    return launch<X, 4, true>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
 }
 
 }  // namespace
@@ -194,13 +465,13 @@ extern "C" int bakron_distill(const void* logits, int dtype, int rows, int vocab
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (dtype) {
         case BAKRON_F32:
-            return launch<BAKRON_F32>(logits, rows, vocab, ld, T, loss, lse, dlogits, ldd,
-                                      dev_status, st);
+            return plan<BAKRON_F32>(logits, rows, vocab, ld, T, loss, lse, dlogits, ldd, dev_status,
+                                    st);
         case BAKRON_F16:
-            return launch<BAKRON_F16>(logits, rows, vocab, ld, T, loss, lse, dlogits, ldd,
-                                      dev_status, st);
+            return plan<BAKRON_F16>(logits, rows, vocab, ld, T, loss, lse, dlogits, ldd, dev_status,
+                                    st);
         default:
-            return launch<BAKRON_BF16>(logits, rows, vocab, ld, T, loss, lse, dlogits, ldd,
-                                       dev_status, st);
+            return plan<BAKRON_BF16>(logits, rows, vocab, ld, T, loss, lse, dlogits, ldd,
+                                     dev_status, st);
     }
 }
