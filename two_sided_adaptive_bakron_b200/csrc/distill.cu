@@ -5,11 +5,12 @@
 //
 // Bound by bytes: a row of the vocabulary read once, and written once with the gradient. A row is
 // shared by a cluster of 1 to 8 blocks, each of which keeps its slice in registers (128 bytes a
-// thread, 64 KB a block, two blocks an SM): all loads of a slice are in flight at once, the maximum
-// and the sum come from one look at it, and the gradient needs no second read. The blocks exchange
-// (maximum, sum) pairs of their warps through distributed shared memory, one barrier a row, and join
-// them in a fixed order. Rows above 512 KB are streamed twice instead (the second time from L2). Few
-// rows are cut finer, so that they fill the GPU.
+// thread, 32 KB a block, four blocks an SM; twice that and two blocks for rows above 256 KB): all
+// loads of a slice are in flight at once, the maximum and the sum come from one look at it, and the
+// gradient needs no second read. One warp goes through the teacher's list meanwhile. The blocks
+// exchange (maximum, sum) pairs of their warps through distributed shared memory, one barrier a row,
+// and join them in a fixed order. Rows above 512 KB are streamed twice instead (the second time from
+// L2). Few rows are cut finer, so that they fill the GPU.
 //
 // All statistics are fp32. Differences from a maximum are taken before they are scaled by 1 / tau, so
 // that nothing large cancels in log p - log q; exponentials are ex2.approx (2 units in the last place).
@@ -25,9 +26,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxK = 1024;
+constexpr int kHash = 2 * kMaxK;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -INFINITY;
 
@@ -62,122 +64,27 @@ __device__ __forceinline__ float logit_at(const Teacher& T, size_t e) {
     return to_f32(static_cast<const __nv_bfloat16*>(T.t)[e]);
 }
 
-// Sum and maximum over the block in a fixed order; every thread gets them.
-__device__ __forceinline__ float block_sum(float v, float* red) {
+// Over a warp, in a fixed order; every lane gets them.
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x / 32] = v;
-    __syncthreads();
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) s += red[k];
-    return s;
+    return v;
 }
-__device__ __forceinline__ float block_max(float v, float* red) {
+__device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x / 32] = v;
-    __syncthreads();
-    float s = kNegInf;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) s = fmaxf(s, red[k]);
-    return s;
+    return v;
 }
-
-// The elements of 16 bytes as fp32 and back, and the larger ones of two vectors (NaN loses).
-template <class X> struct Vec;
-template <> struct Vec<float> {
-    static constexpr int N = 4;
-    static __device__ __forceinline__ void get(const uint4& v, float (&f)[4]) {
-        f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
-        f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
-    }
-    static __device__ __forceinline__ uint4 put(const float (&f)[4]) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                          __float_as_uint(f[3]));
-    }
-    static __device__ __forceinline__ uint4 top(const uint4& a, const uint4& b) {
-        const auto f = [](uint32_t x, uint32_t y) {
-            return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y)));
-        };
-        return make_uint4(f(a.x, b.x), f(a.y, b.y), f(a.z, b.z), f(a.w, b.w));
-    }
-    static __device__ __forceinline__ uint4 fill_low() {
-        return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
-    }
-};
-template <> struct Vec<__half> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void get(const uint4& v, float (&f)[8]) {
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
-            f[2 * k] = p.x, f[2 * k + 1] = p.y;
-        }
-    }
-    static __device__ __forceinline__ uint4 put(const float (&f)[8]) {
-        uint32_t u[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const __half2 p = __floats2half2_rn(f[2 * k], f[2 * k + 1]);
-            u[k] = *reinterpret_cast<const uint32_t*>(&p);
-        }
-        return make_uint4(u[0], u[1], u[2], u[3]);
-    }
-    static __device__ __forceinline__ uint4 top(const uint4& a, const uint4& b) {
-        const auto f = [](uint32_t x, uint32_t y) {
-            const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&x),
-                                      *reinterpret_cast<const __half2*>(&y));
-            return *reinterpret_cast<const uint32_t*>(&m);
-        };
-        return make_uint4(f(a.x, b.x), f(a.y, b.y), f(a.z, b.z), f(a.w, b.w));
-    }
-    static __device__ __forceinline__ uint4 fill_low() {
-        return make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u);
-    }
-};
-template <> struct Vec<__nv_bfloat16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void get(const uint4& v, float (&f)[8]) {
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            f[2 * k] = __uint_as_float(u[k] << 16);
-            f[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
-        }
-    }
-    static __device__ __forceinline__ uint4 put(const float (&f)[8]) {
-        uint32_t u[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-            u[k] = *reinterpret_cast<const uint32_t*>(&p);
-        }
-        return make_uint4(u[0], u[1], u[2], u[3]);
-    }
-    static __device__ __forceinline__ uint4 top(const uint4& a, const uint4& b) {
-        const auto f = [](uint32_t x, uint32_t y) {
-            const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&x),
-                                      *reinterpret_cast<const __nv_bfloat162*>(&y));
-            return *reinterpret_cast<const uint32_t*>(&m);
-        };
-        return make_uint4(f(a.x, b.x), f(a.y, b.y), f(a.z, b.z), f(a.w, b.w));
-    }
-    static __device__ __forceinline__ uint4 fill_low() {
-        return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
-    }
-};
 
 // NV: 16-byte vectors that a thread holds (LOOP: of one round of the stream).
 template <class X, int NV, bool LOOP>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, NV > 8 ? 2 : 4)
 distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict__ loss,
                float* __restrict__ lse, X* dz, int64_t ldd, int* __restrict__ status) {
     constexpr int N = Vec<X>::N;
-    __shared__ float red[kWarps];
+    __shared__ float mass_of_list;
+    __shared__ int twice;                             // an index stands in the list more than once
+    __shared__ int seen[kHash];
     __shared__ float2 pairs[8 * kWarps];              // (maximum, sum) of the cluster's warps
     __shared__ float p[kMaxK], lp[kMaxK], zt[kMaxK];
     __shared__ __align__(16) int at[kMaxK];
@@ -228,35 +135,56 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
     const float zx = extra >= 0 ? to_f32(z[extra]) : kNegInf;
     if (ck > 1) cluster.barrier_arrive();        // (every block has begun: see the exchange)
 
-    // the teacher's list: p, log p and the student's logits there; the first block needs them for
-    // the loss, the others for their part of the gradient
-    float mass = 0.f;
-    if (rank == 0 || dz) {
+    // The teacher's list, by the last warp while the slice arrives: p, log p and the student's
+    // logits there; the first block needs them for the loss, the others for their part of the gradient.
+    const bool list = rank == 0 || dz;
+    const int lane = tid & 31;
+    if (list && T.k > 32) {                       // (a shorter list is compared within the warp)
+        for (int e = tid; e < kHash; e += kThreads) seen[e] = -1;
+        __syncthreads();
+    }
+    if (list && tid >= kThreads - 32) {
         float tmax = kNegInf;
-        for (int j = tid; j < T.k; j += kThreads) {
-            const size_t e = (size_t)row * T.k + j;
-            const long long i = index_at(T, e);
-            const float t = logit_at(T, e);
-            if (i >= V) set_status(status, BAKRON_ERR_INVALID_ARG);
-            const bool there = i >= 0 && i < V && t != kNegInf;
-            at[j] = there ? (int)i : -1;
-            lp[j] = t;
-            zt[j] = there ? to_f32(z[i]) : 0.f;
-            if (there) tmax = fmaxf(tmax, t);
+        bool dup = false;
+        for (int j = lane; j < (T.k + 31) / 32 * 32; j += 32) {
+            int here = -1;
+            if (j < T.k) {
+                const size_t e = (size_t)row * T.k + j;
+                const long long i = index_at(T, e);
+                const float t = logit_at(T, e);
+                if (i >= V) set_status(status, BAKRON_ERR_INVALID_ARG);
+                const bool there = i >= 0 && i < V && t != kNegInf;
+                here = there ? (int)i : -1;
+                lp[j] = t;
+                zt[j] = there ? to_f32(z[i]) : 0.f;
+                if (there) tmax = fmaxf(tmax, t);
+            }
+            if (j < kMaxK) at[j] = here;              // (pads the last four)
+            if (T.k <= 32) {
+                const unsigned same = __match_any_sync(0xffffffffu, here);    // by every lane
+                dup = here >= 0 && __popc(same) > 1;
+            } else if (here >= 0) {
+                unsigned h = (unsigned)here * 2654435761u >> 21;
+                for (int step = 0; step < kHash; ++step, h = (h + 1) % kHash) {
+                    const int was = atomicCAS(&seen[h], -1, here);
+                    dup |= was == here;
+                    if (was == -1 || was == here) break;
+                }
+            }
         }
-        if (tid < 3 && T.k + tid < kMaxK) at[T.k + tid] = -1;      // whole int4s
         float tl = 0.f;      // log p_j = (t_j - tmax) / tau - tl
         if (T.lse) {
             tmax = 0.f;
             tl = T.lse[row];
         } else {
-            tmax = block_max(tmax, red);
-            float s = 0.f;
-            for (int j = tid; j < T.k; j += kThreads)
-                if (at[j] >= 0) s += expf((lp[j] - tmax) * T.inv_tau);
-            tl = logf(block_sum(s, red));
+            tmax = warp_max(tmax);
+            float sum = 0.f;
+            for (int j = lane; j < T.k; j += 32)
+                if (at[j] >= 0) sum += expf((lp[j] - tmax) * T.inv_tau);
+            tl = logf(warp_sum(sum));
         }
-        for (int j = tid; j < T.k; j += kThreads) {
+        float mass = 0.f;
+        for (int j = lane; j < T.k; j += 32) {
             float pj = 0.f;
             if (at[j] >= 0) {
                 lp[j] = (lp[j] - tmax) * T.inv_tau - tl;
@@ -265,7 +193,9 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
             p[j] = pj;
             mass += pj;
         }
-        mass = block_sum(mass, red);
+        mass = warp_sum(mass);
+        dup = __any_sync(0xffffffffu, dup);
+        if (lane == 0) mass_of_list = mass, twice = dup;
     }
 
     // the slice's maximum and sum of 2^(c (z - maximum)), warp by warp
@@ -294,11 +224,6 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
         }
         return (part[0] + part[1]) + (part[2] + part[3]);
     };
-    auto warp_max = [](float a) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        return a;
-    };
     if constexpr (!LOOP) {
         m = warp_max(fmaxf(m, thread_max()));
         s = thread_sum(m);
@@ -315,8 +240,7 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
             load(base);
         }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    s = warp_sum(s);
     if (ck > 1) {
         cluster.barrier_wait();
         if ((tid & 31) < ck)
@@ -337,13 +261,13 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
         else join(m1, s1, m2, s2, c), m = m1, s = s1;
     }
     if (fabsf(m) == INFINITY) s = NAN;      // +inf, or nothing but -inf
-    if (rank == 0) {
+    if (rank == 0 && tid >= kThreads - 32) {
         const float l = logf(s);
         float kl = 0.f;
-        for (int j = tid; j < T.k; j += kThreads)
+        for (int j = lane; j < T.k; j += 32)
             if (p[j] != 0.f) kl += p[j] * (lp[j] - ((zt[j] - m) * T.inv_tau - l));
-        kl = block_sum(kl, red);
-        if (tid == 0) loss[row] = w * kl, lse[row] = m * T.inv_tau + l;
+        kl = warp_sum(kl);
+        if (lane == 0) loss[row] = w * kl, lse[row] = m * T.inv_tau + l;
     }
     if (!dz) return;
 
@@ -352,7 +276,7 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
 #pragma unroll
     for (int u = 0; u < NV; ++u)
         asm volatile("" : "+r"(v[u].x), "+r"(v[u].y), "+r"(v[u].z), "+r"(v[u].w));
-    const float f = w * T.inv_tau;
+    const float f = w * T.inv_tau, mass = mass_of_list;
     const bool none = mass == 0.f;
     const float fq = none ? 0.f : f * mass / s;
     auto grad = [&](float x) { return none ? 0.f : fq * ex2((x - m) * c); };
@@ -382,8 +306,8 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
         if (i < 0) continue;
         const int vec = i < head || i >= V - rest ? -1 : (i - head) / N;
         if (vec < 0 ? rank != 0 : vec < v0 || vec >= v1) continue;
-        float pj = 0.f;              // all entries of this index, in the list's order
-        for (int k = 0; k < T.k; k += 4) {
+        float pj = twice ? 0.f : p[j];   // all entries of this index, in the list's order
+        for (int k = 0; twice && k < T.k; k += 4) {
             const int4 a = *reinterpret_cast<const int4*>(at + k);
             if (a.x == i) pj += p[k];
             if (a.y == i) pj += p[k + 1];
@@ -422,11 +346,11 @@ int plan(const void* z_, int rows, int V, int64_t ld, const Teacher& T, float* l
     const int sms = tc::sm_count();
     if (sms <= 0) return BAKRON_ERR_CUDA;
     // Blocks a row: as many as keep its slices within 8 vectors a thread, and for few rows as
-    // many as fill the GPU twice, as long as a slice has a vector for every thread.
+    // many as fill it (four blocks an SM), as long as a slice has a vector for every thread.
     const int vecs = V / Vec<X>::N;
     int ck = 1;
     while (ck < 8 && vecs > ck * 8 * kThreads) ck *= 2;
-    while (ck < 8 && (long long)rows * ck * 2 <= 2 * sms && vecs > ck * kThreads) ck *= 2;
+    while (ck < 8 && (long long)rows * ck * 2 <= 4 * sms && vecs > ck * kThreads) ck *= 2;
     if ((long long)rows * ck > INT32_MAX) return BAKRON_ERR_INVALID_ARG;
     const int nv = (vecs + ck * kThreads - 1) / (ck * kThreads);
     // a slice is ceil(vecs / ck) vectors at most
@@ -434,6 +358,8 @@ int plan(const void* z_, int rows, int V, int64_t ld, const Teacher& T, float* l
     if (nv <= 2) return launch<X, 2, false>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
     if (nv <= 4) return launch<X, 4, false>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
     if (nv <= 8) return launch<X, 8, false>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
+    if (nv <= 16)
+        return launch<X, 16, false>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
     return launch<X, 4, true>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
 }
 

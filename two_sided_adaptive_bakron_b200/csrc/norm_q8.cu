@@ -3,15 +3,19 @@
 //   h = x + residual, rho = 1 / sqrt(mean h^2 + eps), v = h * weight,
 //   scale_g = max_g |v| rho / 127, q = round_half_even(127 v / max_g |v|)
 //
-// Bound by bytes: x and the residual read once, the sum and the codes written once. One block a row;
-// a thread keeps its elements as they were read (one or two chunks of 8, in registers), so that the
-// codes need no second read. Rows that do not fit (above 16384 elements, 8192 of fp32) are read
-// again, from L2. The blocks of an SM (1024 threads) overlap each other's barriers.
+// Bound by bytes: x and the residual read once, the sum and the codes written once; 7 bytes of a
+// 16-bit element leave about 38 instruction slots of a lane. One block a row, 8 elements (a chunk) a
+// thread and round.
 //
-// rho cancels in the codes, which are those of the real quotient: v and the quotient are fp32 first
-// (relative error below 5 2^-24), and where that leaves the code open -- an element next to its
-// group's maximum, a quotient within 2^-14 of the border of two codes -- fp64 decides, in which the
-// products of 16-bit inputs are exact. One element in 8000 takes the second way.
+// rho cancels in the codes, which are those of the real quotient for the given inputs. So where a
+// group's maximum is known, its codes are: groups of 32, 64, 128 or 256 columns lie within a warp's
+// round, and a row is one pass without a barrier, but for the sum of squares, which only the scales
+// need. Other groups (a whole row) meet in shared memory after a first pass; their elements stay in
+// registers (one or two chunks a thread; longer rows are read again, from L2).
+//
+// v, its maximum and the quotient are fp32: 6 roundings, 4.6e-5 of a code at most. Where that leaves
+// the code open -- within 5e-5 of the border of two codes, one element in 10000 -- fp64 decides, with
+// the group's maximum in fp64; the products of 16-bit inputs are exact there.
 #include <cmath>
 
 #include "lowp.cuh"
@@ -19,9 +23,11 @@
 namespace bakron {
 namespace {
 
-constexpr float kNear = 1.f - 0x1p-20f;      // of the maximum: candidates for it
-constexpr float kBorder = 0.5f - 0x1p-14f;   // from the nearest code: the other one is as near
-constexpr float kTiny = 0x1p-90f;            // below it fp32 quotients lose their relative error
+constexpr float kNear = 1.f - 0x1p-20f;      // of the fp32 maximum: candidates for the exact one
+constexpr float kBorder = 0.5f - 0x1.Ap-15f; // from the nearest code: the next one may be as near
+constexpr float kTiny = 0x1p-90f;            // below it fp32 products lose their relative error
+constexpr float kMagic = 12582912.f;         // 1.5 2^23: adding it leaves the nearest integer (ties
+                                             // to even) in the lowest bits
 
 struct Args {
     const void* x; int64_t ldx; const void* r; int64_t ldr; const void* w; int wd;
@@ -30,28 +36,64 @@ struct Args {
     int wide_x, wide_r, wide_w, wide_sum, wide_q;
 };
 
-// 8 elements from column j on; what lies behind the row is zero.
-template <class X>
-__device__ __forceinline__ void load8(const X* row, int j, int n, bool wide, X (&v)[8]) {
-    if (wide && j + 8 <= n) {
+// 8 neighbouring elements as they stand in memory.
+template <class X> struct Chunk {
+    static constexpr int V = sizeof(X) / 2;
+    uint4 v[V];
+    // from column j on; what lies behind the row is zero
+    __device__ __forceinline__ void load(const X* row, int j, int n, bool wide) {
+        if (wide && j + 8 <= n) {
 #pragma unroll
-        for (int k = 0; k < (int)sizeof(X) / 2; ++k)
-            reinterpret_cast<uint4*>(v)[k] = reinterpret_cast<const uint4*>(row + j)[k];
-    } else {
+            for (int k = 0; k < V; ++k) v[k] = reinterpret_cast<const uint4*>(row + j)[k];
+        } else {
+            __align__(16) X e[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            from_f32(0.f, v[k]);
-            if (j + k < n) v[k] = row[j + k];
+            for (int k = 0; k < 8; ++k) {
+                from_f32(0.f, e[k]);
+                if (j + k < n) e[k] = row[j + k];
+            }
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = reinterpret_cast<const uint4*>(e)[k];
         }
     }
-}
+    __device__ __forceinline__ void store(X* row, int j, int n, bool wide) const {
+        if (wide && j + 8 <= n) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) reinterpret_cast<uint4*>(row + j)[k] = v[k];
+        } else {
+            __align__(16) X e[8];
+#pragma unroll
+            for (int k = 0; k < V; ++k) reinterpret_cast<uint4*>(e)[k] = v[k];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (j + k < n) row[j + k] = e[k];
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            float part[8 / V];
+            Vec<X>::get(v[k], part);
+#pragma unroll
+            for (int c = 0; c < 8 / V; ++c) f[k * (8 / V) + c] = part[c];
+        }
+    }
+    __device__ __forceinline__ void put(const float (&f)[8]) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            float part[8 / V];
+#pragma unroll
+            for (int c = 0; c < 8 / V; ++c) part[c] = f[k * (8 / V) + c];
+            v[k] = Vec<X>::put(part);
+        }
+    }
+};
 
 template <class W>
 __device__ __forceinline__ void weights8(const Args& a, int j, float (&f)[8]) {
-    W w[8];
-    load8<W>(static_cast<const W*>(a.w), j, a.n, a.wide_w, w);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = to_f32(w[k]);
+    Chunk<W> w;
+    w.load(static_cast<const W*>(a.w), j, a.n, a.wide_w);
+    w.get(f);
 }
 __device__ __forceinline__ void weights8(const Args& a, int j, float (&f)[8]) {
     if (!a.w) {
@@ -66,174 +108,285 @@ __device__ __forceinline__ void weights8(const Args& a, int j, float (&f)[8]) {
     }
 }
 
-// C: chunks that a thread keeps (0: none, the row is read again).
+// One row, as a block's threads see it.
+template <class X> struct Row {
+    const Args& a;
+    int64_t row;
+    const X *x, *r;
+    __device__ __forceinline__ explicit Row(const Args& args, int64_t i)
+        : a(args), row(i), x(static_cast<const X*>(args.x) + i * args.ldx),
+          r(args.r ? static_cast<const X*>(args.r) + i * args.ldr : nullptr) {}
+    __device__ __forceinline__ void load(int j, Chunk<X>& xc, Chunk<X>& rc) const {
+        xc.load(x, j, a.n, a.wide_x);
+        if (r) rc.load(r, j, a.n, a.wide_r);
+    }
+    __device__ __forceinline__ void sums(const Chunk<X>& xc, const Chunk<X>& rc,
+                                         float (&h)[8]) const {
+        xc.get(h);
+        if (r) {
+            float f[8];
+            rc.get(f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[k] += f[k];
+        }
+    }
+    __device__ __forceinline__ void put_sum(int j, const float (&h)[8]) const {
+        if (!a.sum || j >= a.n) return;
+        Chunk<X> o;
+        o.put(h);
+        o.store(static_cast<X*>(a.sum) + row * a.lds, j, a.n, a.wide_sum);
+    }
+    // v of the chunk's elements in fp64, one after another: f(k, v)
+    template <class F>
+    __device__ __forceinline__ void exact(int j, const Chunk<X>& xc, const Chunk<X>& rc, F f) const {
+        float xf[8], rf[8], w[8];
+        xc.get(xf);
+        if (r) rc.get(rf);
+        weights8(a, j, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            f(k, (r ? (double)xf[k] + (double)rf[k] : (double)xf[k]) * (double)w[k]);
+    }
+    // Adds the squares of a chunk: in fp32, or in fp64 where they leave its range.
+    __device__ __forceinline__ void squares(const Chunk<X>& xc, const Chunk<X>& rc,
+                                            const float (&h)[8], float& ss, double& far) const {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s = fmaf(h[k], h[k], s);
+        if (s < 0x1p100f && s >= 0x1p-60f) {
+            ss += s;
+        } else {
+            float xf[8], rf[8];
+            xc.get(xf);
+            if (r) rc.get(rf);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const double d = r ? (double)xf[k] + (double)rf[k] : (double)xf[k];
+                far += d * d;
+            }
+        }
+    }
+    // Codes of a chunk for its group's maximum: packed, and whether fp64 has to decide one.
+    static __device__ __forceinline__ bool codes(const float (&v)[8], float top, uint2& out) {
+        const float inv = top < kTiny ? 0.f : 127.f / top;
+        uint32_t bits[8];
+        float far = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float t = v[k] * inv, u = t + kMagic;
+            bits[k] = __float_as_uint(u);
+            far = fmaxf(far, fabsf(t - (u - kMagic)));
+        }
+        out.x = __byte_perm(__byte_perm(bits[0], bits[1], 0x0040),
+                            __byte_perm(bits[2], bits[3], 0x0040), 0x5410);
+        out.y = __byte_perm(__byte_perm(bits[4], bits[5], 0x0040),
+                            __byte_perm(bits[6], bits[7], 0x0040), 0x5410);
+        return far > kBorder || top < kTiny;
+    }
+    __device__ __forceinline__ uint2 exact_codes(int j, const Chunk<X>& xc, const Chunk<X>& rc,
+                                                 double top) const {
+        uint32_t out[2] = {0, 0};
+        if (top > 0.0)
+            exact(j, xc, rc, [&](int k, double v) {
+                out[k / 4] |= ((uint32_t)(int)rint(v * 127.0 / top) & 0xFFu) << (8 * (k % 4));
+            });
+        return make_uint2(out[0], out[1]);
+    }
+    __device__ __forceinline__ void put_codes(int j, uint2 c) const {
+        int8_t* q = a.q + row * a.n + j;
+        if (a.wide_q && j + 8 <= a.n) {
+            *reinterpret_cast<uint2*>(q) = c;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (j + k < a.n) q[k] = (int8_t)((k < 4 ? c.x : c.y) >> (8 * (k % 4)));
+        }
+    }
+};
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The end of a row: scales from the groups' maxima, or a row that is not finite.
+template <int THREADS, class F>
+__device__ __forceinline__ void finish(const Args& a, int64_t row, bool bad, double total, F vmax) {
+    bad |= !(total < INFINITY);
+    if (bad) {
+        for (int j = threadIdx.x; j < a.n; j += THREADS) a.q[row * a.n + j] = 0;
+        if (threadIdx.x == 0 && a.status) set_status(a.status, BAKRON_ERR_NONFINITE);
+    }
+    for (int g = threadIdx.x; g < a.G; g += THREADS)
+        a.scales[row * a.G + g] =
+            bad ? NAN : (float)(vmax(g) / (127.0 * sqrt(total / a.n + (double)a.eps)));
+}
+
+// Groups within a warp's round.
+template <class X, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+norm_q8_groups_kernel(const __grid_constant__ Args a) {
+    extern __shared__ __align__(8) char smem[];
+    double* vmax = reinterpret_cast<double*>(smem);      // of the groups
+    __shared__ double part[THREADS / 32];
+    const Row<X> R(a, blockIdx.x);
+    const int tid = threadIdx.x;
+    float ss = 0.f, nan = 0.f;       // nan: NaN once a v is not finite
+    double far = 0.0;
+    Chunk<X> x0, r0, x1, r1;
+    float w0[8], w1[8];
+    R.load(tid * 8, x0, r0);
+    weights8(a, tid * 8, w0);
+    for (int j0 = 0; j0 < a.n; j0 += THREADS * 8) {
+        const int j = j0 + tid * 8;
+        if (j0 + THREADS * 8 < a.n) {
+            R.load(j + THREADS * 8, x1, r1);
+            weights8(a, j + THREADS * 8, w1);
+        }
+        float h[8], v[8], top = 0.f;
+        R.sums(x0, r0, h);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            v[k] = h[k] * w0[k];
+            nan = fmaf(v[k], 0.f, nan);
+            top = fmaxf(top, fabsf(v[k]));
+        }
+        R.squares(x0, r0, h, ss, far);
+        R.put_sum(j, h);
+        for (int o = 1; o < a.lanes; o <<= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        uint2 c;
+        const bool doubt = Row<X>::codes(v, top, c);
+        double exact_top = (double)top;
+        if (__any_sync(0xffffffffu, doubt && j < a.n)) {
+            // the maximum in fp64, from the elements that may be it
+            const float from = top < kTiny ? 0.f : top * kNear;
+            exact_top = 0.0;
+            R.exact(j, x0, r0, [&](int k, double e) {
+                if (fabsf(v[k]) >= from) exact_top = fmax(exact_top, fabs(e));
+            });
+            for (int o = 1; o < a.lanes; o <<= 1)
+                exact_top = fmax(exact_top, __shfl_xor_sync(0xffffffffu, exact_top, o));
+            if (doubt) c = R.exact_codes(j, x0, r0, exact_top);
+        }
+        if (j < a.n) {
+            R.put_codes(j, c);
+            if ((tid & (a.lanes - 1)) == 0) vmax[j / a.gs] = exact_top;
+        }
+        x0 = x1, r0 = r1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w0[k] = w1[k];
+    }
+    const double s = warp_sum((double)ss + far);
+    if ((tid & 31) == 0) part[tid / 32] = s;
+    const bool bad = __syncthreads_or(!(nan == 0.f));
+    double total = 0.0;
+#pragma unroll
+    for (int k = 0; k < THREADS / 32; ++k) total += part[k];
+    finish<THREADS>(a, R.row, bad, total, [&](int g) { return vmax[g]; });
+}
+
+// Any groups. C: chunks that a thread keeps (0: none, the row is read again).
 template <class X, int C, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 norm_q8_kernel(const __grid_constant__ Args a) {
-    constexpr int K = C > 0 ? C : 1;
+    constexpr int K = C > 0 ? C : 1;      // (indices of kept chunks are constants)
     extern __shared__ __align__(8) char smem[];
     unsigned long long* gmax = reinterpret_cast<unsigned long long*>(smem);   // of doubles >= 0
     unsigned* gmax32 = reinterpret_cast<unsigned*>(gmax + a.G);              // of floats >= 0
     __shared__ double part[THREADS / 32];
-    const int64_t row = blockIdx.x;
+    const Row<X> R(a, blockIdx.x);
     const int tid = threadIdx.x, n = a.n;
-    const X* x = static_cast<const X*>(a.x) + row * a.ldx;
-    const X* r = a.r ? static_cast<const X*>(a.r) + row * a.ldr : nullptr;
     const int rounds = C > 0 ? C : (n + 8 * THREADS - 1) / (8 * THREADS);
-
-    X xv[K][8], rv[K][8];
-    const auto load = [&](int c, X (&xc)[8], X (&rc)[8]) {
-        const int j = (c * THREADS + tid) * 8;
-        load8<X>(x, j, n, a.wide_x, xc);
-        if (r) load8<X>(r, j, n, a.wide_r, rc);
-    };
-    const auto value = [&](const X (&xc)[8], const X (&rc)[8], const float (&w)[8], float (&h)[8],
-                           float (&v)[8]) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            h[k] = r ? to_f32(xc[k]) + to_f32(rc[k]) : to_f32(xc[k]);
-            v[k] = h[k] * w[k];
-        }
-    };
-    const auto exact = [&](X xe, X re, float w) {
-        const double h = r ? (double)to_f32(xe) + (double)to_f32(re) : (double)to_f32(xe);
-        return h * (double)w;
-    };
+    Chunk<X> xc[K], rc[K];
+    float v[K][8], most[K];
+    const auto column = [&](int c) { return (c * THREADS + tid) * 8; };
 
     if (C > 0) {
 #pragma unroll
-        for (int c = 0; c < K; ++c) load(c, xv[c], rv[c]);
+        for (int c = 0; c < K; ++c) R.load(column(c), xc[c], rc[c]);
     }
     for (int g = tid; g < a.G; g += THREADS) gmax[g] = 0, gmax32[g] = 0;
     __syncthreads();
 
-    // sum of squares and the fp32 maxima of the groups
-    float ss = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int c = 0; c < rounds; ++c) {
-        const int b = C > 0 ? c : 0, j = (c * THREADS + tid) * 8;
-        if (C == 0) load(c, xv[b], rv[b]);
-        float w[8], h[8], v[8], top = 0.f;
-        weights8(a, j, w);
-        value(xv[b], rv[b], w, h, v);
+    float ss = 0.f, nan = 0.f;       // nan: NaN once a v is not finite
+    double far = 0.0;
+    const auto values = [&](int c, int b, float (&h)[8]) {
+        float w[8];
+        if (C == 0) R.load(column(c), xc[b], rc[b]);
+        weights8(a, column(c), w);
+        R.sums(xc[b], rc[b], h);
+        most[b] = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            ss = fmaf(h[k], h[k], ss);
-            top = fmaxf(top, fabsf(v[k]));
-            bad |= !(fabsf(h[k]) < INFINITY) || !(fabsf(v[k]) < INFINITY);
+            v[b][k] = h[k] * w[k];
+            most[b] = fmaxf(most[b], fabsf(v[b][k]));
         }
+    };
+#pragma unroll(K)
+    for (int c = 0; c < rounds; ++c) {
+        const int b = C > 0 ? c : 0, j = column(c);
+        float h[8];
+        values(c, b, h);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) nan = fmaf(v[b][k], 0.f, nan);
+        R.squares(xc[b], rc[b], h, ss, far);
+        if (C > 0) R.put_sum(j, h);       // (the elements of this row are all in registers)
+        float top = most[b];
         for (int o = 1; o < a.lanes; o <<= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         if ((tid & (a.lanes - 1)) == 0 && j < n) atomicMax(&gmax32[j / a.gs], __float_as_uint(top));
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if ((tid & 31) == 0) part[tid / 32] = ss;
-    bad = __syncthreads_or(bad);
+    const double s = warp_sum((double)ss + far);
+    if ((tid & 31) == 0) part[tid / 32] = s;
+    const bool bad = __syncthreads_or(!(nan == 0.f));
+
+    // codes; the maxima in fp64 meanwhile, from the elements that may be them
+    unsigned doubt = 0;              // chunks with a code that fp64 decides
+#pragma unroll(K)
+    for (int c = 0; c < rounds; ++c) {
+        const int b = C > 0 ? c : 0, j = column(c);
+        if (j >= n) break;
+        float h[8];
+        if (C == 0) values(c, b, h);
+        const int g = a.G > 1 ? j / a.gs : 0;
+        const float top = __uint_as_float(gmax32[g]), from = top < kTiny ? 0.f : top * kNear;
+        if (most[b] >= from) {
+            double e = 0.0;
+            R.exact(j, xc[b], rc[b], [&](int k, double d) {
+                if (fabsf(v[b][k]) >= from) e = fmax(e, fabs(d));
+            });
+            atomicMax(&gmax[g], (unsigned long long)__double_as_longlong(e));
+        }
+        uint2 q;
+        if (Row<X>::codes(v[b], top, q)) doubt |= 1u << c;
+        R.put_codes(j, q);
+    }
+    __syncthreads();
+#pragma unroll(K)
+    for (int c = 0; c < rounds; ++c) {
+        if (!(doubt >> c & 1)) continue;
+        const int b = C > 0 ? c : 0, j = column(c);
+        if (C == 0) R.load(j, xc[b], rc[b]);
+        R.put_codes(j, R.exact_codes(j, xc[b], rc[b],
+                                     __longlong_as_double((long long)gmax[j / a.gs])));
+    }
+    if (C == 0 && a.sum) {
+        // last, for the sum may take the place of what was read
+        for (int c = 0; c < rounds; ++c) {
+            float h[8];
+            R.load(column(c), xc[0], rc[0]);
+            R.sums(xc[0], rc[0], h);
+            R.put_sum(column(c), h);
+        }
+    }
     double total = 0.0;
 #pragma unroll
     for (int k = 0; k < THREADS / 32; ++k) total += part[k];
-    if (bad) {
-        for (int c = 0; c < rounds; ++c) {
-            const int b = C > 0 ? c : 0, j = (c * THREADS + tid) * 8;
-            if (C == 0) load(c, xv[b], rv[b]);
-            for (int k = 0; k < 8; ++k) {
-                if (j + k >= n) break;
-                const float h = r ? to_f32(xv[b][k]) + to_f32(rv[b][k]) : to_f32(xv[b][k]);
-                a.q[row * n + j + k] = 0;
-                if (a.sum) from_f32(h, static_cast<X*>(a.sum)[row * a.lds + j + k]);
-            }
-        }
-        for (int g = tid; g < a.G; g += THREADS) a.scales[row * a.G + g] = NAN;
-        if (tid == 0 && a.status) set_status(a.status, BAKRON_ERR_NONFINITE);
-        return;
-    }
-    // squares that leave the range of fp32 are added again in fp64
-    if (!(total < 0x1p120) || total < 0x1p-60) {
-        double s = 0.0;
-        for (int c = 0; c < rounds; ++c) {
-            const int b = C > 0 ? c : 0;
-            if (C == 0) load(c, xv[b], rv[b]);
-            for (int k = 0; k < 8; ++k) {
-                const double h = exact(xv[b][k], rv[b][k], 1.f);
-                s += h * h;
-            }
-        }
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        __syncthreads();
-        if ((tid & 31) == 0) part[tid / 32] = s;
-        __syncthreads();
-        total = 0.0;
-        for (int k = 0; k < THREADS / 32; ++k) total += part[k];
-    }
-
-    // the maxima in fp64, from the elements that may be them
-#pragma unroll
-    for (int c = 0; c < rounds; ++c) {
-        const int b = C > 0 ? c : 0, j = (c * THREADS + tid) * 8;
-        if (j >= n) break;
-        if (C == 0) load(c, xv[b], rv[b]);
-        float w[8], h[8], v[8];
-        weights8(a, j, w);
-        value(xv[b], rv[b], w, h, v);
-        const float top = __uint_as_float(gmax32[j / a.gs]);
-        const float from = top < kTiny ? 0.f : top * kNear;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (fabsf(v[k]) >= from)
-                atomicMax(&gmax[j / a.gs], (unsigned long long)__double_as_longlong(
-                                               fabs(exact(xv[b][k], rv[b][k], w[k]))));
-    }
-    __syncthreads();
-
-    // codes, and the sum
-#pragma unroll
-    for (int c = 0; c < rounds; ++c) {
-        const int b = C > 0 ? c : 0, j = (c * THREADS + tid) * 8;
-        if (j >= n) break;
-        if (C == 0) load(c, xv[b], rv[b]);
-        float w[8], h[8], v[8];
-        weights8(a, j, w);
-        value(xv[b], rv[b], w, h, v);
-        const double top = __longlong_as_double((long long)gmax[j / a.gs]);
-        const float inv = (float)(127.0 / top);
-        uint32_t out[2] = {0, 0};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float t = v[k] * inv;
-            float code = rintf(t);
-            if (!(fabsf(t - code) < kBorder) || top < (double)kTiny)
-                code = top > 0.0 ? (float)rint(exact(xv[b][k], rv[b][k], w[k]) * 127.0 / top) : 0.f;
-            out[k / 4] |= ((uint32_t)(int)code & 0xFFu) << (8 * (k % 4));
-        }
-        int8_t* q = a.q + row * n + j;
-        if (a.wide_q && j + 8 <= n) {
-            *reinterpret_cast<uint2*>(q) = make_uint2(out[0], out[1]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (j + k < n) q[k] = (int8_t)(out[k / 4] >> (8 * (k % 4)));
-        }
-        if (a.sum) {
-            X* s = static_cast<X*>(a.sum) + row * a.lds + j;
-            __align__(16) X o[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) from_f32(h[k], o[k]);
-            if (a.wide_sum && j + 8 <= n) {
-#pragma unroll
-                for (int k = 0; k < (int)sizeof(X) / 2; ++k)
-                    reinterpret_cast<uint4*>(s)[k] = reinterpret_cast<const uint4*>(o)[k];
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (j + k < n) s[k] = o[k];
-            }
-        }
-    }
-    const double rho = 1.0 / sqrt(total / n + (double)a.eps);
-    for (int g = tid; g < a.G; g += THREADS)
-        a.scales[row * a.G + g] = (float)(__longlong_as_double((long long)gmax[g]) * rho / 127.0);
+    if (bad || !(total < INFINITY)) __syncthreads();     // (the codes are overwritten by others)
+    finish<THREADS>(a, R.row, bad, total,
+                    [&](int g) { return __longlong_as_double((long long)gmax[g]); });
 }
 
 template <class X, int C, int THREADS>
@@ -242,20 +395,39 @@ int launch(const Args& a, int rows, cudaStream_t st) {
     count_launches(1);
     return cuda_err(cudaGetLastError());
 }
+template <class X, int THREADS>
+int launch_groups(const Args& a, int rows, cudaStream_t st) {
+    norm_q8_groups_kernel<X, THREADS><<<rows, THREADS, (size_t)a.G * 8, st>>>(a);
+    count_launches(1);
+    return cuda_err(cudaGetLastError());
+}
 
-// Threads and chunks by the row's length: one chunk a thread as long as blocks stay small, two where
-// they are 16-bit values (8 registers a chunk; fp32 takes 16), nothing kept above 1024 threads' worth.
+// Threads by the row's length: a block of up to 512 threads goes over a row of groups in rounds, with
+// the next one's loads ahead. Where a row meets in shared memory, one chunk a thread as long as
+// blocks stay small, two where they are 16-bit values (fp32 takes twice the registers), nothing kept
+// above 1024 threads' worth.
 template <int D>
 int plan(const Args& a, int rows, cudaStream_t st) {
     using X = typename Elem<D>::T;
     constexpr bool half = sizeof(X) == 2;
     const int chunks = (a.n + 7) / 8;
+    if (a.G > 1 && 256 % a.gs == 0) {
+        if (chunks <= 64) return launch_groups<X, 64>(a, rows, st);
+        if (chunks <= 128) return launch_groups<X, 128>(a, rows, st);
+        if (chunks <= 512) return launch_groups<X, 256>(a, rows, st);
+        return launch_groups<X, 512>(a, rows, st);
+    }
     if (chunks <= 64) return launch<X, 1, 64>(a, rows, st);
     if (chunks <= 128) return launch<X, 1, 128>(a, rows, st);
     if (chunks <= 256) return launch<X, 1, 256>(a, rows, st);
-    if (chunks <= 512) return half ? launch<X, half ? 2 : 0, 256>(a, rows, st) : launch<X, 1, 512>(a, rows, st);
-    if (chunks <= 1024) return half ? launch<X, half ? 2 : 0, 512>(a, rows, st) : launch<X, 1, 1024>(a, rows, st);
-    if (half && chunks <= 2048) return launch<X, half ? 2 : 0, 1024>(a, rows, st);
+    if (half) {
+        if (chunks <= 512) return launch<X, half ? 2 : 0, 256>(a, rows, st);
+        if (chunks <= 1024) return launch<X, half ? 2 : 0, 512>(a, rows, st);
+        if (chunks <= 2048) return launch<X, half ? 2 : 0, 1024>(a, rows, st);
+    } else {
+        if (chunks <= 512) return launch<X, half ? 0 : 1, 512>(a, rows, st);
+        if (chunks <= 1024) return launch<X, half ? 0 : 1, 1024>(a, rows, st);
+    }
     return launch<X, 0, 1024>(a, rows, st);
 }
 
