@@ -13,9 +13,10 @@
 // need. Other groups (a whole row) meet in shared memory after a first pass; their elements stay in
 // registers (one or two chunks a thread; longer rows are read again, from L2).
 //
-// v, its maximum and the quotient are fp32: 6 roundings, 4.6e-5 of a code at most. Where that leaves
-// the code open -- within 5e-5 of the border of two codes, one element in 10000 -- fp64 decides, with
-// the group's maximum in fp64; the products of 16-bit inputs are exact there.
+// v, its maximum and the quotient are fp32 (two roundings each of v and the maximum, two for the
+// reciprocal, two products: 8 2^-24, 6.1e-5 of a code at most). Where that leaves the code open --
+// within 2^-14 of the border of two codes, one element in 8000 -- fp64 decides, with the group's
+// maximum in fp64; the products of 16-bit inputs are exact there.
 #include <cmath>
 
 #include "lowp.cuh"
@@ -24,8 +25,9 @@ namespace bakron {
 namespace {
 
 constexpr float kNear = 1.f - 0x1p-20f;      // of the fp32 maximum: candidates for the exact one
-constexpr float kBorder = 0.5f - 0x1.Ap-15f; // from the nearest code: the next one may be as near
-constexpr float kTiny = 0x1p-90f;            // below it fp32 products lose their relative error
+constexpr float kBorder = 0.5f - 0x1p-14f;   // from the nearest code: the next one may be as near
+constexpr float kTiny = 0x1p-90f;            // below it fp32 products lose their relative error,
+constexpr float kHuge = 0x1p120f;            // above it reciprocals do
 constexpr float kMagic = 12582912.f;         // 1.5 2^23: adding it leaves the nearest integer (ties
                                              // to even) in the lowest bits
 
@@ -33,16 +35,20 @@ struct Args {
     const void* x; int64_t ldx; const void* r; int64_t ldr; const void* w; int wd;
     int n; float eps; int gs, G, lanes;   // lanes: of a warp that share a group, a power of two
     int8_t* q; float* scales; void* sum; int64_t lds; int* status;
-    int wide_x, wide_r, wide_w, wide_sum, wide_q;
+    int wide_x, wide_r, wide_w, wide_sum, wide_q, same_w;
 };
 
-// 8 neighbouring elements as they stand in memory.
-template <class X> struct Chunk {
+// 8 neighbouring elements as they stand in memory. WIDE: rows of whole, aligned chunks.
+template <class X, bool WIDE> struct Elements {
     static constexpr int V = sizeof(X) / 2;
     uint4 v[V];
     // from column j on; what lies behind the row is zero
     __device__ __forceinline__ void load(const X* row, int j, int n, bool wide) {
-        if (wide && j + 8 <= n) {
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                v[k] = j < n ? reinterpret_cast<const uint4*>(row + j)[k] : make_uint4(0, 0, 0, 0);
+        } else if (wide && j + 8 <= n) {
 #pragma unroll
             for (int k = 0; k < V; ++k) v[k] = reinterpret_cast<const uint4*>(row + j)[k];
         } else {
@@ -57,7 +63,7 @@ template <class X> struct Chunk {
         }
     }
     __device__ __forceinline__ void store(X* row, int j, int n, bool wide) const {
-        if (wide && j + 8 <= n) {
+        if (WIDE || (wide && j + 8 <= n)) {
 #pragma unroll
             for (int k = 0; k < V; ++k) reinterpret_cast<uint4*>(row + j)[k] = v[k];
         } else {
@@ -91,7 +97,7 @@ template <class X> struct Chunk {
 
 template <class W>
 __device__ __forceinline__ void weights8(const Args& a, int j, float (&f)[8]) {
-    Chunk<W> w;
+    Elements<W, false> w;
     w.load(static_cast<const W*>(a.w), j, a.n, a.wide_w);
     w.get(f);
 }
@@ -108,19 +114,32 @@ __device__ __forceinline__ void weights8(const Args& a, int j, float (&f)[8]) {
     }
 }
 
+// Weights of x's type are loaded ahead as they stand, others where they are used.
+template <class X, bool WIDE>
+__device__ __forceinline__ void weights_ahead(const Args& a, int j, Elements<X, WIDE>& w) {
+    if (WIDE || a.same_w) w.load(static_cast<const X*>(a.w), j, a.n, a.wide_w);
+}
+template <class X, bool WIDE>
+__device__ __forceinline__ void weights8(const Args& a, int j, const Elements<X, WIDE>& w,
+                                         float (&f)[8]) {
+    if (WIDE || a.same_w) w.get(f);
+    else weights8(a, j, f);
+}
+
 // One row, as a block's threads see it.
-template <class X> struct Row {
+template <class X, bool WIDE> struct Row {
+    using Chunk = Elements<X, WIDE>;
     const Args& a;
     int64_t row;
     const X *x, *r;
     __device__ __forceinline__ explicit Row(const Args& args, int64_t i)
         : a(args), row(i), x(static_cast<const X*>(args.x) + i * args.ldx),
           r(args.r ? static_cast<const X*>(args.r) + i * args.ldr : nullptr) {}
-    __device__ __forceinline__ void load(int j, Chunk<X>& xc, Chunk<X>& rc) const {
+    __device__ __forceinline__ void load(int j, Chunk& xc, Chunk& rc) const {
         xc.load(x, j, a.n, a.wide_x);
         if (r) rc.load(r, j, a.n, a.wide_r);
     }
-    __device__ __forceinline__ void sums(const Chunk<X>& xc, const Chunk<X>& rc,
+    __device__ __forceinline__ void sums(const Chunk& xc, const Chunk& rc,
                                          float (&h)[8]) const {
         xc.get(h);
         if (r) {
@@ -132,13 +151,13 @@ template <class X> struct Row {
     }
     __device__ __forceinline__ void put_sum(int j, const float (&h)[8]) const {
         if (!a.sum || j >= a.n) return;
-        Chunk<X> o;
+        Chunk o;
         o.put(h);
         o.store(static_cast<X*>(a.sum) + row * a.lds, j, a.n, a.wide_sum);
     }
     // v of the chunk's elements in fp64, one after another: f(k, v)
     template <class F>
-    __device__ __forceinline__ void exact(int j, const Chunk<X>& xc, const Chunk<X>& rc, F f) const {
+    __device__ __forceinline__ void exact(int j, const Chunk& xc, const Chunk& rc, F f) const {
         float xf[8], rf[8], w[8];
         xc.get(xf);
         if (r) rc.get(rf);
@@ -148,7 +167,7 @@ template <class X> struct Row {
             f(k, (r ? (double)xf[k] + (double)rf[k] : (double)xf[k]) * (double)w[k]);
     }
     // Adds the squares of a chunk: in fp32, or in fp64 where they leave its range.
-    __device__ __forceinline__ void squares(const Chunk<X>& xc, const Chunk<X>& rc,
+    __device__ __forceinline__ void squares(const Chunk& xc, const Chunk& rc,
                                             const float (&h)[8], float& ss, double& far) const {
         float s = 0.f;
 #pragma unroll
@@ -166,24 +185,30 @@ template <class X> struct Row {
             }
         }
     }
-    // Codes of a chunk for its group's maximum: packed, and whether fp64 has to decide one.
+    // Codes of a chunk for its group's maximum: packed, and whether fp64 has to decide one (also
+    // where a v is not finite: NaN wins in `far`).
     static __device__ __forceinline__ bool codes(const float (&v)[8], float top, uint2& out) {
-        const float inv = top < kTiny ? 0.f : 127.f / top;
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(top));
+        inv *= 127.f;
+        const bool usual = top >= kTiny && top <= kHuge;
+        if (!usual) inv = top * 0.f;
         uint32_t bits[8];
         float far = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const float t = v[k] * inv, u = t + kMagic;
             bits[k] = __float_as_uint(u);
-            far = fmaxf(far, fabsf(t - (u - kMagic)));
+            const float d = fabsf(t - (u - kMagic));
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(far) : "f"(d));
         }
         out.x = __byte_perm(__byte_perm(bits[0], bits[1], 0x0040),
                             __byte_perm(bits[2], bits[3], 0x0040), 0x5410);
         out.y = __byte_perm(__byte_perm(bits[4], bits[5], 0x0040),
                             __byte_perm(bits[6], bits[7], 0x0040), 0x5410);
-        return far > kBorder || top < kTiny;
+        return !(far <= kBorder) || !usual;
     }
-    __device__ __forceinline__ uint2 exact_codes(int j, const Chunk<X>& xc, const Chunk<X>& rc,
+    __device__ __forceinline__ uint2 exact_codes(int j, const Chunk& xc, const Chunk& rc,
                                                  double top) const {
         uint32_t out[2] = {0, 0};
         if (top > 0.0)
@@ -194,7 +219,7 @@ template <class X> struct Row {
     }
     __device__ __forceinline__ void put_codes(int j, uint2 c) const {
         int8_t* q = a.q + row * a.n + j;
-        if (a.wide_q && j + 8 <= a.n) {
+        if (WIDE || (a.wide_q && j + 8 <= a.n)) {
             *reinterpret_cast<uint2*>(q) = c;
         } else {
 #pragma unroll
@@ -204,52 +229,84 @@ template <class X> struct Row {
     }
 };
 
-__device__ __forceinline__ double warp_sum(double v) {
+template <class T>
+__device__ __forceinline__ T warp_sum(T v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// The end of a row: scales from the groups' maxima, or a row that is not finite.
+// The end of a row, by all threads: the sum of squares (fp32 parts, fp64 ones where there are any)
+// and the scales from the groups' maxima, or a row that is not finite: codes 0, scales NaN.
 template <int THREADS, class F>
-__device__ __forceinline__ void finish(const Args& a, int64_t row, bool bad, double total, F vmax) {
-    bad |= !(total < INFINITY);
-    if (bad) {
-        for (int j = threadIdx.x; j < a.n; j += THREADS) a.q[row * a.n + j] = 0;
-        if (threadIdx.x == 0 && a.status) set_status(a.status, BAKRON_ERR_NONFINITE);
+__device__ __forceinline__ void finish(const Args& a, int64_t row, bool nan, float ss, double far,
+                                       double* part64, float* part, F vmax) {
+    const int tid = threadIdx.x;
+    ss = warp_sum(ss);
+    if ((tid & 31) == 0) part[tid / 32] = ss;
+    const bool odd = __syncthreads_or(nan || far != 0.0 || !(ss < INFINITY));
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < THREADS / 32; ++k) t += part[k];
+    if (!odd) {
+        const float s = 127.f * sqrtf(t / (float)a.n + a.eps);
+        for (int g = tid; g < a.G; g += THREADS) {
+            const double v = vmax(g);
+            a.scales[row * a.G + g] = v < (double)kTiny ? (float)(v / (double)s) : (float)v / s;
+        }
+        return;
     }
-    for (int g = threadIdx.x; g < a.G; g += THREADS)
-        a.scales[row * a.G + g] =
-            bad ? NAN : (float)(vmax(g) / (127.0 * sqrt(total / a.n + (double)a.eps)));
+    far = warp_sum(far);
+    if ((tid & 31) == 0) part64[tid / 32] = far;
+    nan = __syncthreads_or(nan);
+    double total = t;
+    for (int k = 0; k < THREADS / 32; ++k) total += part64[k];
+    if (nan || !(total < INFINITY)) {
+        for (int j = tid; j < a.n; j += THREADS) a.q[row * a.n + j] = 0;
+        for (int g = tid; g < a.G; g += THREADS) a.scales[row * a.G + g] = NAN;
+        if (tid == 0 && a.status) set_status(a.status, BAKRON_ERR_NONFINITE);
+        return;
+    }
+    for (int g = tid; g < a.G; g += THREADS)
+        a.scales[row * a.G + g] = (float)(vmax(g) / (127.0 * sqrt(total / a.n + (double)a.eps)));
+}
+
+__device__ __forceinline__ bool any_not_finite(const float (&v)[8]) {
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bad |= !(fabsf(v[k]) < INFINITY);
+    return bad;
 }
 
 // Groups within a warp's round.
-template <class X, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+template <class X, int THREADS, bool WIDE>
+__global__ void __launch_bounds__(THREADS, THREADS > 512 ? 1 : 768 / THREADS)
 norm_q8_groups_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(8) char smem[];
     double* vmax = reinterpret_cast<double*>(smem);      // of the groups
-    __shared__ double part[THREADS / 32];
-    const Row<X> R(a, blockIdx.x);
+    __shared__ double part64[THREADS / 32];
+    __shared__ float part[THREADS / 32];
+    using Rw = Row<X, WIDE>;
+    const Rw R(a, blockIdx.x);
     const int tid = threadIdx.x;
-    float ss = 0.f, nan = 0.f;       // nan: NaN once a v is not finite
+    bool nan = false;                // whether a v is not finite
+    float ss = 0.f;
     double far = 0.0;
-    Chunk<X> x0, r0, x1, r1;
-    float w0[8], w1[8];
+    typename Rw::Chunk x0, r0, w0, x1, r1, w1;
     R.load(tid * 8, x0, r0);
-    weights8(a, tid * 8, w0);
+    weights_ahead(a, tid * 8, w0);
     for (int j0 = 0; j0 < a.n; j0 += THREADS * 8) {
         const int j = j0 + tid * 8;
         if (j0 + THREADS * 8 < a.n) {
             R.load(j + THREADS * 8, x1, r1);
-            weights8(a, j + THREADS * 8, w1);
+            weights_ahead(a, j + THREADS * 8, w1);
         }
-        float h[8], v[8], top = 0.f;
+        float h[8], w[8], v[8], top = 0.f;
         R.sums(x0, r0, h);
+        weights8(a, j, w0, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            v[k] = h[k] * w0[k];
-            nan = fmaf(v[k], 0.f, nan);
+            v[k] = h[k] * w[k];
             top = fmaxf(top, fabsf(v[k]));
         }
         R.squares(x0, r0, h, ss, far);
@@ -257,7 +314,7 @@ norm_q8_groups_kernel(const __grid_constant__ Args a) {
         for (int o = 1; o < a.lanes; o <<= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         uint2 c;
-        const bool doubt = Row<X>::codes(v, top, c);
+        const bool doubt = Rw::codes(v, top, c);
         double exact_top = (double)top;
         if (__any_sync(0xffffffffu, doubt && j < a.n)) {
             // the maximum in fp64, from the elements that may be it
@@ -268,38 +325,32 @@ norm_q8_groups_kernel(const __grid_constant__ Args a) {
             });
             for (int o = 1; o < a.lanes; o <<= 1)
                 exact_top = fmax(exact_top, __shfl_xor_sync(0xffffffffu, exact_top, o));
-            if (doubt) c = R.exact_codes(j, x0, r0, exact_top);
+            if (doubt) nan |= any_not_finite(v), c = R.exact_codes(j, x0, r0, exact_top);
         }
         if (j < a.n) {
             R.put_codes(j, c);
             if ((tid & (a.lanes - 1)) == 0) vmax[j / a.gs] = exact_top;
         }
-        x0 = x1, r0 = r1;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w0[k] = w1[k];
+        x0 = x1, r0 = r1, w0 = w1;
     }
-    const double s = warp_sum((double)ss + far);
-    if ((tid & 31) == 0) part[tid / 32] = s;
-    const bool bad = __syncthreads_or(!(nan == 0.f));
-    double total = 0.0;
-#pragma unroll
-    for (int k = 0; k < THREADS / 32; ++k) total += part[k];
-    finish<THREADS>(a, R.row, bad, total, [&](int g) { return vmax[g]; });
+    finish<THREADS>(a, R.row, nan, ss, far, part64, part, [&](int g) { return vmax[g]; });
 }
 
 // Any groups. C: chunks that a thread keeps (0: none, the row is read again).
-template <class X, int C, int THREADS>
+template <class X, int C, int THREADS, bool WIDE>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 norm_q8_kernel(const __grid_constant__ Args a) {
     constexpr int K = C > 0 ? C : 1;      // (indices of kept chunks are constants)
     extern __shared__ __align__(8) char smem[];
     unsigned long long* gmax = reinterpret_cast<unsigned long long*>(smem);   // of doubles >= 0
     unsigned* gmax32 = reinterpret_cast<unsigned*>(gmax + a.G);              // of floats >= 0
-    __shared__ double part[THREADS / 32];
-    const Row<X> R(a, blockIdx.x);
+    __shared__ double part64[THREADS / 32];
+    __shared__ float part[THREADS / 32];
+    using Rw = Row<X, WIDE>;
+    const Rw R(a, blockIdx.x);
     const int tid = threadIdx.x, n = a.n;
     const int rounds = C > 0 ? C : (n + 8 * THREADS - 1) / (8 * THREADS);
-    Chunk<X> xc[K], rc[K];
+    typename Rw::Chunk xc[K], rc[K];
     float v[K][8], most[K];
     const auto column = [&](int c) { return (c * THREADS + tid) * 8; };
 
@@ -310,7 +361,8 @@ norm_q8_kernel(const __grid_constant__ Args a) {
     for (int g = tid; g < a.G; g += THREADS) gmax[g] = 0, gmax32[g] = 0;
     __syncthreads();
 
-    float ss = 0.f, nan = 0.f;       // nan: NaN once a v is not finite
+    bool nan = false;                // whether a v is not finite
+    float ss = 0.f;
     double far = 0.0;
     const auto values = [&](int c, int b, float (&h)[8]) {
         float w[8];
@@ -329,8 +381,6 @@ norm_q8_kernel(const __grid_constant__ Args a) {
         const int b = C > 0 ? c : 0, j = column(c);
         float h[8];
         values(c, b, h);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) nan = fmaf(v[b][k], 0.f, nan);
         R.squares(xc[b], rc[b], h, ss, far);
         if (C > 0) R.put_sum(j, h);       // (the elements of this row are all in registers)
         float top = most[b];
@@ -338,9 +388,7 @@ norm_q8_kernel(const __grid_constant__ Args a) {
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         if ((tid & (a.lanes - 1)) == 0 && j < n) atomicMax(&gmax32[j / a.gs], __float_as_uint(top));
     }
-    const double s = warp_sum((double)ss + far);
-    if ((tid & 31) == 0) part[tid / 32] = s;
-    const bool bad = __syncthreads_or(!(nan == 0.f));
+    __syncthreads();
 
     // codes; the maxima in fp64 meanwhile, from the elements that may be them
     unsigned doubt = 0;              // chunks with a code that fp64 decides
@@ -360,7 +408,7 @@ norm_q8_kernel(const __grid_constant__ Args a) {
             atomicMax(&gmax[g], (unsigned long long)__double_as_longlong(e));
         }
         uint2 q;
-        if (Row<X>::codes(v[b], top, q)) doubt |= 1u << c;
+        if (Rw::codes(v[b], top, q)) doubt |= 1u << c, nan |= any_not_finite(v[b]);
         R.put_codes(j, q);
     }
     __syncthreads();
@@ -381,54 +429,57 @@ norm_q8_kernel(const __grid_constant__ Args a) {
             R.put_sum(column(c), h);
         }
     }
-    double total = 0.0;
-#pragma unroll
-    for (int k = 0; k < THREADS / 32; ++k) total += part[k];
-    if (bad || !(total < INFINITY)) __syncthreads();     // (the codes are overwritten by others)
-    finish<THREADS>(a, R.row, bad, total,
+    finish<THREADS>(a, R.row, nan, ss, far, part64, part,
                     [&](int g) { return __longlong_as_double((long long)gmax[g]); });
 }
 
-template <class X, int C, int THREADS>
+template <class X, int C, int THREADS, bool WIDE>
 int launch(const Args& a, int rows, cudaStream_t st) {
-    norm_q8_kernel<X, C, THREADS><<<rows, THREADS, (size_t)a.G * 12, st>>>(a);
+    norm_q8_kernel<X, C, THREADS, WIDE><<<rows, THREADS, (size_t)a.G * 12, st>>>(a);
     count_launches(1);
     return cuda_err(cudaGetLastError());
 }
-template <class X, int THREADS>
+template <class X, int THREADS, bool WIDE>
 int launch_groups(const Args& a, int rows, cudaStream_t st) {
-    norm_q8_groups_kernel<X, THREADS><<<rows, THREADS, (size_t)a.G * 8, st>>>(a);
+    norm_q8_groups_kernel<X, THREADS, WIDE><<<rows, THREADS, (size_t)a.G * 8, st>>>(a);
     count_launches(1);
     return cuda_err(cudaGetLastError());
 }
 
-// Threads by the row's length: a block of up to 512 threads goes over a row of groups in rounds, with
-// the next one's loads ahead. Where a row meets in shared memory, one chunk a thread as long as
+// Threads by the row's length: a block goes over a row of groups in rounds, with the next one's loads
+// ahead. Where a row meets in shared memory, one chunk a thread as long as
 // blocks stay small, two where they are 16-bit values (fp32 takes twice the registers), nothing kept
 // above 1024 threads' worth.
-template <int D>
+template <class X, bool WIDE>
 int plan(const Args& a, int rows, cudaStream_t st) {
-    using X = typename Elem<D>::T;
     constexpr bool half = sizeof(X) == 2;
     const int chunks = (a.n + 7) / 8;
     if (a.G > 1 && 256 % a.gs == 0) {
-        if (chunks <= 64) return launch_groups<X, 64>(a, rows, st);
-        if (chunks <= 128) return launch_groups<X, 128>(a, rows, st);
-        if (chunks <= 512) return launch_groups<X, 256>(a, rows, st);
-        return launch_groups<X, 512>(a, rows, st);
+        // many rows: long rounds of small blocks; few rows: as many threads as help one row
+        if (chunks <= 64) return launch_groups<X, 64, WIDE>(a, rows, st);
+        if (chunks <= 128 || rows >= 4 * 148) return launch_groups<X, 128, WIDE>(a, rows, st);
+        return launch_groups<X, 512, WIDE>(a, rows, st);
     }
-    if (chunks <= 64) return launch<X, 1, 64>(a, rows, st);
-    if (chunks <= 128) return launch<X, 1, 128>(a, rows, st);
-    if (chunks <= 256) return launch<X, 1, 256>(a, rows, st);
+    if (chunks <= 64) return launch<X, 1, 64, WIDE>(a, rows, st);
+    if (chunks <= 128) return launch<X, 1, 128, WIDE>(a, rows, st);
+    if (chunks <= 256) return launch<X, 1, 256, WIDE>(a, rows, st);
     if (half) {
-        if (chunks <= 512) return launch<X, half ? 2 : 0, 256>(a, rows, st);
-        if (chunks <= 1024) return launch<X, half ? 2 : 0, 512>(a, rows, st);
-        if (chunks <= 2048) return launch<X, half ? 2 : 0, 1024>(a, rows, st);
+        if (chunks <= 512) return launch<X, half ? 2 : 0, 256, WIDE>(a, rows, st);
+        if (chunks <= 1024) return launch<X, half ? 2 : 0, 512, WIDE>(a, rows, st);
+        if (chunks <= 2048) return launch<X, half ? 2 : 0, 1024, WIDE>(a, rows, st);
     } else {
-        if (chunks <= 512) return launch<X, half ? 0 : 1, 512>(a, rows, st);
-        if (chunks <= 1024) return launch<X, half ? 0 : 1, 1024>(a, rows, st);
+        if (chunks <= 512) return launch<X, half ? 0 : 1, 512, WIDE>(a, rows, st);
+        if (chunks <= 1024) return launch<X, half ? 0 : 1, 1024, WIDE>(a, rows, st);
     }
-    return launch<X, 0, 1024>(a, rows, st);
+    return launch<X, 0, 1024, WIDE>(a, rows, st);
+}
+
+template <int D>
+int plan(const Args& a, int rows, cudaStream_t st) {
+    using X = typename Elem<D>::T;
+    const bool wide = a.n % 8 == 0 && a.wide_x && (!a.r || a.wide_r) && a.wide_w && a.same_w &&
+                      (!a.sum || a.wide_sum) && a.wide_q;
+    return wide ? plan<X, true>(a, rows, st) : plan<X, false>(a, rows, st);
 }
 
 }  // namespace
@@ -463,6 +514,7 @@ extern "C" int bakron_rms_norm_q8(const void* x, int64_t ldx, const void* residu
     a.wide_r = rows16(residual, ldr);
     a.wide_sum = rows16(sum, lds);
     a.wide_w = weight && aligned_to(weight, 16);
+    a.same_w = weight && weight_dtype == dtype;
     a.wide_q = n % 8 == 0 && aligned_to(q, 8);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (dtype) {
