@@ -112,4 +112,4 @@ def test_binding_refuses_what_the_library_cannot_see(bk):
         bk._steps(8, 0)
     meta = torch.zeros(4, 64, device="meta")
     with pytest.raises(ValueError, match="CUDA"):
-        bk._rows(meta, "x")
+        bk._rows(meta, "x", meta.get_device())

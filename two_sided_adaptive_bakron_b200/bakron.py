@@ -286,29 +286,34 @@ def bakron_row_scales(W, group_size, divisor, scales, stream=None) -> int:
 # The entry points below are called once a layer and token, so their binding is kept short: sizes
 # and strides are read once, the library checks them, and only what it cannot see (device, type,
 # a strided last dimension, the length of a buffer) is checked here.
-def _rows(t: torch.Tensor, name: str):
-    """(rows, columns, row stride) of a 1-D or 2-D CUDA tensor whose last stride is 1."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() == 1:
-        if t.numel() > 1 and t.stride(0) != 1:
-            raise ValueError(f"{name}: the last dimension must have stride 1")
-        return 1, t.shape[0], t.shape[0]
-    if t.dim() != 2:
+def _rows(t: torch.Tensor, name: str, device: int):
+    """(rows, columns, row stride) of a 1-D or 2-D tensor on ``device`` whose last stride is 1."""
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{device}" if device >= 0
+                                                            else ""))
+    dim = t.dim()
+    if dim == 2:
+        r, c = t.shape
+        ld, inner = t.stride()
+        if r <= 1:
+            ld = c
+        if (c > 1 and inner != 1) or ld < c:
+            raise ValueError(f"{name}: expected rows of stride-1 elements that do not overlap, got "
+                             f"strides {tuple(t.stride())}")
+        return r, c, ld
+    if dim != 1:
         raise ValueError(f"{name}: expected one or two dimensions, got {tuple(t.shape)}")
-    r, c = t.shape
-    if c > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the last dimension must have stride 1")
-    ld = t.stride(0) if r > 1 else c
-    if ld < c:
-        raise ValueError(f"{name}: rows must not overlap")
-    return r, c, ld
+    c = t.shape[0]
+    if c > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name}: expected stride-1 elements, got {tuple(t.stride())}")
+    return 1, c, c
 
 
-def _flat(t, dtype, numel: int, name: str, device) -> int:
+def _flat(t, dtype, numel: int, name: str, device: int) -> int:
     """Data pointer of a contiguous tensor of a given type and length on ``device``."""
-    if t.dtype != dtype or t.numel() != numel or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected {numel} contiguous {dtype} on {device}, got "
+    if t.dtype != dtype or t.numel() != numel or t.get_device() != device or \
+            not t.is_contiguous():
+        raise ValueError(f"{name}: expected {numel} contiguous {dtype} on cuda:{device}, got "
                          f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} on "
                          f"{t.device}")
     return t.data_ptr()
@@ -321,23 +326,27 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return d
 
 
-def _call(fn, device, stream, *args) -> int:
-    """fn(*args, stream) with ``device`` current: the library launches on the current device."""
-    i = device.index
-    if i == torch.cuda.current_device():
-        st = _raw_stream(i) if stream is None else _stream(stream)
-        return fn(*args, st)
-    with torch.cuda.device(i):
-        return fn(*args, _raw_stream(i) if stream is None else _stream(stream))
-
-
-def _raw_stream(index: int) -> int:
+def _current_stream(index: int) -> int:
     return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same handle without building a Stream object, where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
+def _call(fn, device: int, stream, *args) -> int:
+    """fn(*args, stream) with ``device`` current: the library launches on the current device."""
+    if device == torch.cuda.current_device():
+        return fn(*args, _raw_stream(device) if stream is None else _stream(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _raw_stream(device) if stream is None else _stream(stream))
 
 
 def _steps(n: int, group_size) -> tuple[int, int]:
     """(columns per step, steps per row); None is one step per row."""
-    g = n if group_size is None else int(group_size)
+    if group_size is None:
+        return n, 1
+    g = int(group_size)
     if g < 1:
         raise ValueError(f"group_size must be positive, got {group_size}")
     return g, (1 if g >= n else -(-n // g))
@@ -348,7 +357,7 @@ def _codebook(codebook):
     if codebook is None:
         return None, 0
     if not isinstance(codebook, ctypes.Array):
-        codebook = (ctypes.c_float * len(codebook))(*[float(v) for v in codebook])
+        codebook = (ctypes.c_float * len(codebook))(*codebook)
     bits = len(codebook).bit_length() - 1
     if len(codebook) != 1 << bits or not 1 <= bits <= 4:
         raise ValueError(f"a codebook has 2, 4, 8 or 16 entries, got {len(codebook)}")
@@ -361,26 +370,28 @@ def bakron_pack4_bytes(m: int, n: int, group_size: int) -> int:
 
 def bakron_pack4(codes, scales, group_size, unsigned_codes, packed, dev_status,
                  stream=None) -> int:
-    m, n, ldc = _rows(codes, "codes")
+    dev = codes.get_device()
+    m, n, ldc = _rows(codes, "codes", dev)
     if codes.dtype != torch.int8:
         raise ValueError(f"codes: expected torch.int8, got {codes.dtype}")
-    dev = codes.device
     g, G = _steps(n, group_size)
-    return _call(lib().bakron_pack4, dev, stream, codes.data_ptr(), ldc,
+    L = lib()
+    return _call(L.bakron_pack4, dev, stream, codes.data_ptr(), ldc,
                  _flat(scales, torch.float32, m * G, "scales", dev), m, n, g,
                  int(bool(unsigned_codes)),
-                 _flat(packed, torch.uint8, bakron_pack4_bytes(m, n, g), "packed", dev),
+                 _flat(packed, torch.uint8, L.bakron_pack4_bytes(m, n, g), "packed", dev),
                  _flat(dev_status, torch.int32, 1, "dev_status", dev))
 
 
 def bakron_unpack4(packed, group_size, unsigned_codes, codes, scales, stream=None) -> int:
-    m, n, ldc = _rows(codes, "codes")
+    dev = codes.get_device()
+    m, n, ldc = _rows(codes, "codes", dev)
     if codes.dtype != torch.int8:
         raise ValueError(f"codes: expected torch.int8, got {codes.dtype}")
-    dev = codes.device
     g, G = _steps(n, group_size)
-    return _call(lib().bakron_unpack4, dev, stream,
-                 _flat(packed, torch.uint8, bakron_pack4_bytes(m, n, g), "packed", dev), m, n, g,
+    L = lib()
+    return _call(L.bakron_unpack4, dev, stream,
+                 _flat(packed, torch.uint8, L.bakron_pack4_bytes(m, n, g), "packed", dev), m, n, g,
                  int(bool(unsigned_codes)), codes.data_ptr(), ldc,
                  _flat(scales, torch.float32, m * G, "scales", dev))
 
@@ -389,17 +400,22 @@ def bakron_matvec4(packed, group_size, codebook, x, x_scales, x_group_size, y,
                    stream=None) -> int:
     """``x``: tokens x n (or n), ``y``: tokens x m (or m); ``codebook``: None, a sequence or a
     ctypes float array."""
-    tokens, n, ldx = _rows(x, "x")
-    rows, m, ldy = _rows(y, "y")
-    dev = x.device
-    if rows != tokens or y.device != dev:
-        raise ValueError(f"y: expected {tokens} rows on {dev}, got {tuple(y.shape)} on {y.device}")
+    dev = x.get_device()
+    rows, m, ldy = _rows(y, "y", dev)
+    if rows != (1 if x.dim() == 1 else x.shape[0]):
+        raise ValueError(f"y: expected the rows of x, got {tuple(y.shape)}")
+    return _matvec4(packed, m, group_size, codebook, x, x_scales, x_group_size, y, ldy, dev, stream)
+
+
+def _matvec4(packed, m, group_size, codebook, x, x_scales, x_group_size, y, ldy, dev, stream):
+    """bakron_matvec4 for a y that is known to have the rows of x, m columns and stride ldy."""
+    tokens, n, ldx = _rows(x, "x", dev)
     g, _ = _steps(n, group_size)
     L = lib()
     nbytes = L.bakron_pack4_bytes(m, n, g)
     if nbytes == 0:
         return BAKRON_ERR_INVALID_ARG
-    cb, bits = _codebook(codebook)
+    cb, bits = (None, 0) if codebook is None else _codebook(codebook)
     gx, xs = n, None
     if x_scales is not None:
         gx, Gx = _steps(n, x_group_size)
@@ -411,43 +427,63 @@ def bakron_matvec4(packed, group_size, codebook, x, x_scales, x_group_size, y,
 
 def bakron_rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out=None,
                        dev_status=None, stream=None) -> int:
-    rows, n, ldx = _rows(x, "x")
-    dev = x.device
-    g, G = _steps(n, group_size)
-    ldr = lds = 0
-    rp = wp = sp = None
-    wd = 0
-    if residual is not None:
-        rr, rn, ldr = _rows(residual, "residual")
-        if (rr, rn) != (rows, n) or residual.dtype != x.dtype or residual.device != dev:
-            raise ValueError("residual: expected the shape, type and device of x")
-        rp = residual.data_ptr()
+    dev = x.get_device()
+    rows, n, _ = _rows(x, "x", dev)
+    _, G = _steps(n, group_size)
+    lds = 0
     if sum_out is not None:
-        sr, sn, lds = _rows(sum_out, "sum_out")
-        if (sr, sn) != (rows, n) or sum_out.dtype != x.dtype or sum_out.device != dev:
-            raise ValueError("sum_out: expected the shape, type and device of x")
-        sp = sum_out.data_ptr()
+        sr, sn, lds = _rows(sum_out, "sum_out", dev)
+        if sr != rows or sn != n or sum_out.dtype != x.dtype:
+            raise ValueError("sum_out: expected the shape and type of x")
+    _flat(q, torch.int8, rows * n, "q", dev)
+    _flat(scales, torch.float32, rows * G, "scales", dev)
+    return _rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out, lds, dev_status,
+                        dev, stream)
+
+
+def _rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out, lds, dev_status, dev,
+                 stream):
+    """bakron_rms_norm_q8 for outputs that are known to fit."""
+    rows, n, ldx = _rows(x, "x", dev)
+    dt = x.dtype
+    ldr = wd = 0
+    rp = wp = None
+    if residual is not None:
+        rr, rn, ldr = _rows(residual, "residual", dev)
+        if rr != rows or rn != n or residual.dtype != dt:
+            raise ValueError("residual: expected the shape and type of x")
+        rp = residual.data_ptr()
     if weight is not None:
-        wp = _flat(weight, weight.dtype, n, "weight", dev)
         wd = _dtype(weight, "weight")
-    st = None if dev_status is None else _flat(dev_status, torch.int32, 1, "dev_status", dev)
+        wp = _flat(weight, weight.dtype, n, "weight", dev)
     return _call(lib().bakron_rms_norm_q8, dev, stream, x.data_ptr(), ldx, rp, ldr,
-                 _dtype(x, "x"), wp, wd, rows, n, float(eps), g,
-                 _flat(q, torch.int8, rows * n, "q", dev),
-                 _flat(scales, torch.float32, rows * G, "scales", dev), sp, lds, st)
+                 _dtype(x, "x"), wp, wd, rows, n, eps, n if group_size is None else group_size,
+                 q.data_ptr(), scales.data_ptr(),
+                 None if sum_out is None else sum_out.data_ptr(), lds,
+                 None if dev_status is None else
+                 _flat(dev_status, torch.int32, 1, "dev_status", dev))
 
 
 def bakron_distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature, loss, lse,
                    dlogits, dev_status, stream=None) -> int:
-    rows, V, ld = _rows(logits, "logits")
-    dev = logits.device
-    k = top_idx.shape[-1]
-    ldd, dp = 0, None
+    dev = logits.get_device()
+    rows, V, _ = _rows(logits, "logits", dev)
+    ldd = 0
     if dlogits is not None:
-        dr, dv, ldd = _rows(dlogits, "dlogits")
-        if (dr, dv) != (rows, V) or dlogits.dtype != logits.dtype or dlogits.device != dev:
-            raise ValueError("dlogits: expected the shape, type and device of logits")
-        dp = dlogits.data_ptr()
+        dr, dv, ldd = _rows(dlogits, "dlogits", dev)
+        if dr != rows or dv != V or dlogits.dtype != logits.dtype:
+            raise ValueError("dlogits: expected the shape and type of logits")
+    _flat(loss, torch.float32, rows, "loss", dev)
+    _flat(lse, torch.float32, rows, "lse", dev)
+    return _distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature, loss, lse,
+                    dlogits, ldd, dev_status, dev, stream)
+
+
+def _distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature, loss, lse, dlogits,
+             ldd, dev_status, dev, stream):
+    """bakron_distill for outputs that are known to fit."""
+    rows, V, ld = _rows(logits, "logits", dev)
+    k = top_idx.shape[-1]
     return _call(lib().bakron_distill, dev, stream, logits.data_ptr(), _dtype(logits, "logits"),
                  rows, V, ld, _flat(top_idx, top_idx.dtype, rows * k, "top_idx", dev),
                  _dtype(top_idx, "top_idx"),
@@ -457,8 +493,8 @@ def bakron_distill(logits, top_idx, top_logits, teacher_lse, row_weights, temper
                  _flat(teacher_lse, torch.float32, rows, "teacher_lse", dev),
                  None if row_weights is None else
                  _flat(row_weights, torch.float32, rows, "row_weights", dev),
-                 float(temperature), _flat(loss, torch.float32, rows, "loss", dev),
-                 _flat(lse, torch.float32, rows, "lse", dev), dp, ldd,
+                 temperature, loss.data_ptr(), lse.data_ptr(),
+                 None if dlogits is None else dlogits.data_ptr(), ldd,
                  _flat(dev_status, torch.int32, 1, "dev_status", dev))
 
 
@@ -627,7 +663,9 @@ def proxy_loss(dW, H_O, H_I, stream=None) -> torch.Tensor:
 
 def _status_of(status, device, check: bool):
     """(status word, whether to read it): the caller's own word is left to the caller."""
-    return (new_status(device), check) if status is None else (status, False)
+    if status is not None:
+        return status, False
+    return new_status(device), check
 
 
 def pack4(codes, scales, group_size=None, unsigned: bool = False, stream=None,
@@ -635,12 +673,12 @@ def pack4(codes, scales, group_size=None, unsigned: bool = False, stream=None,
     """The 4-bit layout of a layer's codes (m x n int8) and grid steps (m, or m x G with a
     group size); ``unsigned`` for codebook indices. With the caller's own ``status`` word the
     call does not wait for the device."""
-    m, n, _ = _rows(codes, "codes")
+    m, n = codes.shape
     g, _ = _steps(n, group_size)
     nbytes = bakron_pack4_bytes(m, n, g)
     if nbytes == 0:
         raise BakronError(BAKRON_ERR_INVALID_ARG, "bakron_pack4")
-    packed = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+    packed = codes.new_empty(nbytes, dtype=torch.uint8)
     st, read = _status_of(status, codes.device, check)
     _raise(bakron_pack4(codes, scales, g, unsigned, packed, st, stream), "bakron_pack4")
     if read:
@@ -651,9 +689,8 @@ def pack4(codes, scales, group_size=None, unsigned: bool = False, stream=None,
 def unpack4(packed, m: int, n: int, group_size=None, unsigned: bool = False, stream=None):
     """(codes, scales) of a layer in the 4-bit layout; scales m, or m x G with a group size."""
     _, G = _steps(n, group_size)
-    codes = torch.empty((m, n), dtype=torch.int8, device=packed.device)
-    scales = torch.empty((m,) if group_size is None else (m, G), dtype=torch.float32,
-                         device=packed.device)
+    codes = packed.new_empty((m, n), dtype=torch.int8)
+    scales = packed.new_empty((m,) if group_size is None else (m, G), dtype=torch.float32)
     _raise(bakron_unpack4(packed, group_size, unsigned, codes, scales, stream), "bakron_unpack4")
     return codes, scales
 
@@ -662,13 +699,16 @@ def matvec4(packed, m: int, n: int, x, group_size=None, codebook=None, x_scales=
             x_group_size=None, out_dtype=None, stream=None) -> torch.Tensor:
     """y = x W^T for a layer (m x n) in the 4-bit layout and x of one token (n) or a few (tokens x
     n); y has x's type (float32 for int8 x) unless ``out_dtype`` names another."""
-    if x.shape[-1] != n:
-        raise ValueError(f"x: expected {n} columns, got {tuple(x.shape)}")
+    shape = x.shape
+    if shape[-1] != n:
+        raise ValueError(f"x: expected {n} columns, got {tuple(shape)}")
     if out_dtype is None:
         out_dtype = torch.float32 if x.dtype == torch.int8 else x.dtype
-    y = torch.empty(x.shape[:-1] + (m,), dtype=out_dtype, device=x.device)
-    _raise(bakron_matvec4(packed, group_size, codebook, x, x_scales, x_group_size, y, stream),
-           "bakron_matvec4")
+    y = x.new_empty((shape[0], m) if len(shape) == 2 else (m,), dtype=out_dtype)
+    code = _matvec4(packed, m, group_size, codebook, x, x_scales, x_group_size, y, m,
+                    x.get_device(), stream)
+    if code:
+        raise BakronError(code, "bakron_matvec4")
     return y
 
 
@@ -678,15 +718,20 @@ def rms_norm_q8(x, weight=None, eps: float = 1e-6, residual=None, group_size=Non
     without a residual, unless ``sum_out`` asks for it). Scales: one per row, or rows x G with a
     group size. Rows that are not finite give NaN scales and, where the caller gives a ``status``
     word, BAKRON_ERR_NONFINITE in it."""
-    n = x.shape[-1]
-    _, G = _steps(n, group_size)
-    lead = x.shape[:-1]
-    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-    scales = torch.empty(lead + (G,), dtype=torch.float32, device=x.device)
-    if sum_out is None and residual is not None:
-        sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _raise(bakron_rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out, status,
-                              stream), "bakron_rms_norm_q8")
+    shape = x.shape
+    _, G = _steps(shape[-1], group_size)
+    q = x.new_empty(shape, dtype=torch.int8)
+    scales = x.new_empty((shape[0], G) if len(shape) == 2 else (G,), dtype=torch.float32)
+    if sum_out is not None:
+        code = bakron_rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out, status,
+                                  stream)
+    else:
+        if residual is not None:
+            sum_out = x.new_empty(shape)
+        code = _rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out, shape[-1],
+                            status, x.get_device(), stream)
+    if code:
+        raise BakronError(code, "bakron_rms_norm_q8")
     return q, scales, sum_out
 
 
@@ -697,16 +742,20 @@ def distill(logits, top_idx, top_logits, temperature: float = 1.0, teacher_lse=N
     the student's log-sum-exp of logits / temperature, and the gradient of the summed loss (None
     unless ``grad``; ``dlogits`` names its buffer, which may be ``logits``). With the caller's own
     ``status`` word the call does not wait for the device."""
-    rows = 1 if logits.dim() == 1 else logits.shape[0]
-    loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    lse = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    if not grad:
-        dlogits = None
-    elif dlogits is None:
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    st, read = _status_of(status, logits.device, check)
-    _raise(bakron_distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature,
-                          loss, lse, dlogits, st, stream), "bakron_distill")
+    shape = logits.shape
+    rows = 1 if len(shape) == 1 else shape[0]
+    loss = logits.new_empty(rows, dtype=torch.float32)
+    lse = logits.new_empty(rows, dtype=torch.float32)
+    st, read = (status, False) if status is not None else _status_of(None, logits.device, check)
+    if grad and dlogits is not None:
+        code = bakron_distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature,
+                              loss, lse, dlogits, st, stream)
+    else:
+        dlogits = logits.new_empty(shape) if grad else None
+        code = _distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature, loss,
+                        lse, dlogits, shape[-1], st, logits.get_device(), stream)
+    if code:
+        raise BakronError(code, "bakron_distill")
     if read:
         _raise(bakron_read_status(st, stream), "bakron_distill (device)")
     return loss, lse, dlogits
