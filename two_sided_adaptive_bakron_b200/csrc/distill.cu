@@ -3,19 +3,25 @@
 //   q = softmax(z / tau),  p_j = exp(t_j / tau - T),
 //   loss = w sum_j p_j (log p_j - log q_{i_j}),   dz_i = (w / tau) (M q_i - sum_{j: i_j = i} p_j)
 //
-// Bound by bytes: a row of the vocabulary read once, and written once with the gradient. A row is
-// shared by a cluster of 1 to 8 blocks, each of which keeps its slice in registers (128 bytes a
-// thread, 32 KB a block, four blocks an SM; twice that and two blocks for rows above 256 KB): all
-// loads of a slice are in flight at once, the maximum and the sum come from one look at it, and the
-// gradient needs no second read. One warp goes through the teacher's list meanwhile. The blocks
-// exchange (maximum, sum) pairs of their warps through distributed shared memory, one barrier a row,
-// and join them in a fixed order. Rows above 512 KB are streamed twice instead (the second time from
-// L2). Few rows are cut finer, so that they fill the GPU.
+// Bound by bytes: a row of the vocabulary read once, and written once with the gradient. What stands
+// against it is the chain of a row: its list (index, then the logit there), its statistics, a
+// barrier, and only then its gradient; about 5 us, in which an SM could move 200 KB. So:
+//
+//   * Many rows (distill_rows_kernel): blocks stay on the GPU and go from row to row. A thread keeps
+//     its first vectors of a row in shared memory, brought there by cp.async during the row before (as
+//     soon as that row's own are written out); what does not fit is streamed, and read again from
+//     L2 for the gradient. One warp goes through the teacher's lists a row ahead. The barriers are
+//     named ones: between the data warps, and between them and the list's warp.
+//   * Few rows (distill_kernel): a row is shared by a cluster of up to 8 blocks, so that the rows fill
+//     the GPU; each block keeps its slice in registers (rows above 512 KB are streamed twice). The
+//     blocks exchange (maximum, sum) pairs of their warps through distributed shared memory and join
+//     them in a fixed order.
 //
 // All statistics are fp32. Differences from a maximum are taken before they are scaled by 1 / tau, so
 // that nothing large cancels in log p - log q; exponentials are ex2.approx (2 units in the last place).
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "lowp.cuh"
@@ -76,6 +82,130 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
+// What is kept of a teacher's list: p, log p, the student's logits, the indices (-1: absent; padded
+// to whole int4s), a table to find indices that stand there twice (lists above 32 entries), sum p.
+struct List {
+    float *p, *lp, *zt; int *at, *seen; float* mass; int* twice;
+};
+
+// A row's list, by one warp.
+template <class X>
+__device__ __forceinline__ void read_list(const Teacher& T, const X* z, int row, int V,
+                                          const List& L, int* status) {
+    const int lane = threadIdx.x & 31;
+    if (T.k > 32) {
+        for (int e = lane; e < kHash; e += 32) L.seen[e] = -1;
+        __syncwarp();
+    }
+    float tmax = kNegInf;
+    bool dup = false;
+    for (int j = lane; j < (T.k + 31) / 32 * 32; j += 32) {
+        int here = -1;
+        if (j < T.k) {
+            const size_t e = (size_t)row * T.k + j;
+            const long long i = index_at(T, e);
+            const float t = logit_at(T, e);
+            if (i >= V) set_status(status, BAKRON_ERR_INVALID_ARG);
+            const bool there = i >= 0 && i < V && t != kNegInf;
+            here = there ? (int)i : -1;
+            L.lp[j] = t;
+            L.zt[j] = there ? to_f32(z[i]) : 0.f;
+            if (there) tmax = fmaxf(tmax, t);
+        }
+        if (j < (T.k + 3) / 4 * 4) L.at[j] = here;
+        if (T.k <= 32) {
+            const unsigned same = __match_any_sync(0xffffffffu, here);    // by every lane
+            dup = here >= 0 && __popc(same) > 1;
+        } else if (here >= 0) {
+            unsigned h = (unsigned)here * 2654435761u >> 21;
+            for (int step = 0; step < kHash; ++step, h = (h + 1) % kHash) {
+                const int was = atomicCAS(&L.seen[h], -1, here);
+                dup |= was == here;
+                if (was == -1 || was == here) break;
+            }
+        }
+    }
+    __syncwarp();
+    float tl = 0.f;      // log p_j = (t_j - tmax) / tau - tl
+    if (T.lse) {
+        tmax = 0.f;
+        tl = T.lse[row];
+    } else {
+        tmax = warp_max(tmax);
+        float sum = 0.f;
+        for (int j = lane; j < T.k; j += 32)
+            if (L.at[j] >= 0) sum += expf((L.lp[j] - tmax) * T.inv_tau);
+        tl = logf(warp_sum(sum));
+    }
+    float mass = 0.f;
+    for (int j = lane; j < T.k; j += 32) {
+        float pj = 0.f;
+        if (L.at[j] >= 0) {
+            L.lp[j] = (L.lp[j] - tmax) * T.inv_tau - tl;
+            pj = expf(L.lp[j]);
+        }
+        L.p[j] = pj;
+        mass += pj;
+    }
+    mass = warp_sum(mass);
+    dup = __any_sync(0xffffffffu, dup);
+    if (lane == 0) *L.mass = mass, *L.twice = dup;
+}
+
+// The loss of a row, by one warp, from the list and the row's (m, s).
+__device__ __forceinline__ float list_loss(const Teacher& T, const List& L, float m, float l) {
+    float kl = 0.f;
+    for (int j = threadIdx.x & 31; j < T.k; j += 32)
+        if (L.p[j] != 0.f) kl += L.p[j] * (L.lp[j] - ((L.zt[j] - m) * T.inv_tau - l));
+    return warp_sum(kl);
+}
+
+// Sum of p over all entries of entry j's index, in the list's order.
+__device__ __forceinline__ float list_p(const Teacher& T, const List& L, int j) {
+    if (!*L.twice) return L.p[j];
+    const int i = L.at[j];
+    float pj = 0.f;
+    for (int k = 0; k < T.k; k += 4) {
+        const int4 a = *reinterpret_cast<const int4*>(L.at + k);
+        if (a.x == i) pj += L.p[k];
+        if (a.y == i) pj += L.p[k + 1];
+        if (a.z == i) pj += L.p[k + 2];
+        if (a.w == i) pj += L.p[k + 3];
+    }
+    return pj;
+}
+
+// Joins the pairs of a block's or cluster's warps, every warp for itself and all alike.
+__device__ __forceinline__ void join_pairs(const float2* pairs, int count, float c, float& m,
+                                           float& s) {
+    const int lane = threadIdx.x & 31;
+    m = kNegInf, s = 0.f;
+    for (int k = lane; k < count; k += 32) join(m, s, pairs[k].x, pairs[k].y, c);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        // both lanes of a pair join in the same order
+        float m1 = m, s1 = s, m2 = __shfl_xor_sync(0xffffffffu, m, o),
+              s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane & o) join(m2, s2, m1, s1, c), m = m2, s = s2;
+        else join(m1, s1, m2, s2, c), m = m1, s = s1;
+    }
+    if (fabsf(m) == INFINITY) s = NAN;      // +inf, or nothing but -inf
+}
+
+// How a row lies to 16-byte boundaries: `head` elements, `body` vectors, `rest` elements.
+template <class X> struct Span {
+    int head, body, rest;
+    __device__ __forceinline__ Span(const X* z, int V) {
+        head = min(V, (int)((16 - reinterpret_cast<uintptr_t>(z) % 16) % 16 / sizeof(X)));
+        body = (V - head) / Vec<X>::N;
+        rest = V - head - body * Vec<X>::N;
+    }
+    // the element outside the vectors that thread tid takes, or -1
+    __device__ __forceinline__ int extra(int tid, int V) const {
+        return tid < head ? tid : tid >= 32 && tid < 32 + rest ? V - rest + tid - 32 : -1;
+    }
+};
+
 // NV: 16-byte vectors that a thread holds (LOOP: of one round of the stream).
 template <class X, int NV, bool LOOP>
 __global__ void __launch_bounds__(kThreads, NV > 8 ? 2 : 4)
@@ -83,11 +213,12 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
                float* __restrict__ lse, X* dz, int64_t ldd, int* __restrict__ status) {
     constexpr int N = Vec<X>::N;
     __shared__ float mass_of_list;
-    __shared__ int twice;                             // an index stands in the list more than once
+    __shared__ int twice;
     __shared__ int seen[kHash];
     __shared__ float2 pairs[8 * kWarps];              // (maximum, sum) of the cluster's warps
     __shared__ float p[kMaxK], lp[kMaxK], zt[kMaxK];
     __shared__ __align__(16) int at[kMaxK];
+    const List L{p, lp, zt, at, seen, &mass_of_list, &twice};
     cg::cluster_group cluster = cg::this_cluster();
     const int ck = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int row = blockIdx.x / ck, tid = threadIdx.x;
@@ -97,11 +228,10 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
 
     // The row: `head` elements up to a 16-byte boundary, `body` vectors, the rest. The blocks
     // share the vectors; head and rest (16 elements at most) are the first block's, one a thread.
-    const int head = min(V, (int)((16 - reinterpret_cast<uintptr_t>(z) % 16) % 16 / sizeof(X)));
-    const int body = (V - head) / N, rest = V - head - body * N;
+    const Span<X> S(z, V);
+    const int head = S.head, body = S.body, rest = S.rest;
     const int v0 = (int)((long long)body * rank / ck), v1 = (int)((long long)body * (rank + 1) / ck);
-    int extra = -1;
-    if (rank == 0) extra = tid < head ? tid : tid >= 32 && tid < 32 + rest ? V - rest + tid - 32 : -1;
+    const int extra = rank == 0 ? S.extra(tid, V) : -1;
     const uint4* zv = reinterpret_cast<const uint4*>(z + head);
     // the gradient's row may lie otherwise to the boundaries: element by element then
     const bool wide = reinterpret_cast<uintptr_t>(dz + head) % 16 == 0;
@@ -135,68 +265,12 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
     const float zx = extra >= 0 ? to_f32(z[extra]) : kNegInf;
     if (ck > 1) cluster.barrier_arrive();        // (every block has begun: see the exchange)
 
-    // The teacher's list, by the last warp while the slice arrives: p, log p and the student's
-    // logits there; the first block needs them for the loss, the others for their part of the gradient.
+    // The teacher's list, by the last warp while the slice arrives; the first block needs it for the
+    // loss, the others for their part of the gradient.
     const bool list = rank == 0 || dz;
     const int lane = tid & 31;
-    if (list && T.k > 32) {                       // (a shorter list is compared within the warp)
-        for (int e = tid; e < kHash; e += kThreads) seen[e] = -1;
-        __syncthreads();
-    }
-    if (list && tid >= kThreads - 32) {
-        float tmax = kNegInf;
-        bool dup = false;
-        for (int j = lane; j < (T.k + 31) / 32 * 32; j += 32) {
-            int here = -1;
-            if (j < T.k) {
-                const size_t e = (size_t)row * T.k + j;
-                const long long i = index_at(T, e);
-                const float t = logit_at(T, e);
-                if (i >= V) set_status(status, BAKRON_ERR_INVALID_ARG);
-                const bool there = i >= 0 && i < V && t != kNegInf;
-                here = there ? (int)i : -1;
-                lp[j] = t;
-                zt[j] = there ? to_f32(z[i]) : 0.f;
-                if (there) tmax = fmaxf(tmax, t);
-            }
-            if (j < kMaxK) at[j] = here;              // (pads the last four)
-            if (T.k <= 32) {
-                const unsigned same = __match_any_sync(0xffffffffu, here);    // by every lane
-                dup = here >= 0 && __popc(same) > 1;
-            } else if (here >= 0) {
-                unsigned h = (unsigned)here * 2654435761u >> 21;
-                for (int step = 0; step < kHash; ++step, h = (h + 1) % kHash) {
-                    const int was = atomicCAS(&seen[h], -1, here);
-                    dup |= was == here;
-                    if (was == -1 || was == here) break;
-                }
-            }
-        }
-        float tl = 0.f;      // log p_j = (t_j - tmax) / tau - tl
-        if (T.lse) {
-            tmax = 0.f;
-            tl = T.lse[row];
-        } else {
-            tmax = warp_max(tmax);
-            float sum = 0.f;
-            for (int j = lane; j < T.k; j += 32)
-                if (at[j] >= 0) sum += expf((lp[j] - tmax) * T.inv_tau);
-            tl = logf(warp_sum(sum));
-        }
-        float mass = 0.f;
-        for (int j = lane; j < T.k; j += 32) {
-            float pj = 0.f;
-            if (at[j] >= 0) {
-                lp[j] = (lp[j] - tmax) * T.inv_tau - tl;
-                pj = expf(lp[j]);
-            }
-            p[j] = pj;
-            mass += pj;
-        }
-        mass = warp_sum(mass);
-        dup = __any_sync(0xffffffffu, dup);
-        if (lane == 0) mass_of_list = mass, twice = dup;
-    }
+    if (list && tid >= kThreads - 32)
+        read_list<X>(T, z, row, V, L, status);
 
     // the slice's maximum and sum of 2^(c (z - maximum)), warp by warp
     const float c = T.inv_tau * kLog2e;
@@ -250,23 +324,10 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
         if ((tid & 31) == 0) pairs[tid / 32] = make_float2(m, s);
         __syncthreads();
     }
-    m = kNegInf, s = 0.f;
-    for (int k = tid & 31; k < ck * kWarps; k += 32) join(m, s, pairs[k].x, pairs[k].y, c);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        // both lanes of a pair join in the same order
-        float m1 = m, s1 = s, m2 = __shfl_xor_sync(0xffffffffu, m, o),
-              s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        if (tid & o) join(m2, s2, m1, s1, c), m = m2, s = s2;
-        else join(m1, s1, m2, s2, c), m = m1, s = s1;
-    }
-    if (fabsf(m) == INFINITY) s = NAN;      // +inf, or nothing but -inf
+    join_pairs(pairs, ck * kWarps, c, m, s);
     if (rank == 0 && tid >= kThreads - 32) {
         const float l = logf(s);
-        float kl = 0.f;
-        for (int j = lane; j < T.k; j += 32)
-            if (p[j] != 0.f) kl += p[j] * (lp[j] - ((zt[j] - m) * T.inv_tau - l));
-        kl = warp_sum(kl);
+        const float kl = list_loss(T, L, m, l);
         if (lane == 0) loss[row] = w * kl, lse[row] = m * T.inv_tau + l;
     }
     if (!dz) return;
@@ -306,15 +367,193 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
         if (i < 0) continue;
         const int vec = i < head || i >= V - rest ? -1 : (i - head) / N;
         if (vec < 0 ? rank != 0 : vec < v0 || vec >= v1) continue;
-        float pj = twice ? 0.f : p[j];   // all entries of this index, in the list's order
-        for (int k = 0; twice && k < T.k; k += 4) {
-            const int4 a = *reinterpret_cast<const int4*>(at + k);
-            if (a.x == i) pj += p[k];
-            if (a.y == i) pj += p[k + 1];
-            if (a.z == i) pj += p[k + 2];
-            if (a.w == i) pj += p[k + 3];
+        from_f32(fq * ex2((zt[j] - m) * c) - f * list_p(T, L, j), dz[i]);
+    }
+}
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Blocks that go from row to row: DATA threads and a warp for the lists. `keep`: vectors of a row
+// that a thread keeps in shared memory.
+template <class X, int DATA, bool GRAD>
+__global__ void __launch_bounds__(DATA + 32, 1024 / DATA)
+distill_rows_kernel(const X* z0, int rows, int V, int64_t ld, const Teacher T,
+                    float* __restrict__ loss, float* __restrict__ lse, X* dz0, int64_t ldd,
+                    int* __restrict__ status, int keep) {
+    constexpr int N = Vec<X>::N, ALL = DATA + 32;
+    enum { kData = 1, kListReady = 2, kListFree = 4 };      // barriers (the last two: one a buffer)
+    extern __shared__ __align__(16) char smem[];
+    __shared__ float2 pairs[2][DATA / 32];
+    __shared__ float mass_of_list[2];
+    __shared__ int twice[2];
+    const int tid = threadIdx.x, lane = tid & 31, step = gridDim.x;
+    const int k4 = (T.k + 3) / 4 * 4;
+    float* lists = reinterpret_cast<float*>(smem + (size_t)keep * DATA * 16);
+    const auto list = [&](int b) {
+        float* l = lists + b * 4 * k4;
+        return List{l, l + k4, l + 2 * k4, reinterpret_cast<int*>(l + 3 * k4),
+                    reinterpret_cast<int*>(lists + 8 * k4), &mass_of_list[b], &twice[b]};
+    };
+
+    if (tid >= DATA) {
+        for (int row = blockIdx.x, it = 0; row < rows; row += step, ++it) {
+            if (it >= 2) bar_sync(kListFree + (it & 1), ALL);
+            if (!T.w || T.w[row] != 0.f)
+                read_list<X>(T, z0 + (int64_t)row * ld, row, V, list(it & 1), status);
+            __syncwarp();
+            bar_arrive(kListReady + (it & 1), ALL);
         }
-        from_f32(fq * ex2((zt[j] - m) * c) - f * pj, dz[i]);
+        return;
+    }
+
+    const float c = T.inv_tau * kLog2e;
+    uint4* slot = reinterpret_cast<uint4*>(smem) + tid;
+    const uint32_t slot32 = (uint32_t)__cvta_generic_to_shared(slot);
+    const auto weight = [&](int row) { return row < rows ? T.w ? T.w[row] : 1.f : 0.f; };
+    // starts the copies of the vectors that are kept of a row
+    const auto prefetch = [&](int row, float w) {
+        if (w != 0.f) {
+            const X* z = z0 + (int64_t)row * ld;
+            const Span<X> S(z, V);
+            const uint4* zv = reinterpret_cast<const uint4*>(z + S.head) + tid;
+            for (int u = 0; u < keep && u * DATA + tid < S.body; ++u)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot32 +
+                                                                               u * DATA * 16),
+                             "l"(zv + u * DATA)
+                             : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    float w = weight(blockIdx.x);
+    prefetch(blockIdx.x, w);
+    for (int row = blockIdx.x, it = 0; row < rows; row += step, ++it) {
+        const int b = it & 1;
+        const X* z = z0 + (int64_t)row * ld;
+        X* dz = GRAD ? dz0 + (int64_t)row * ldd : nullptr;
+        const Span<X> S(z, V);
+        const int extra = S.extra(tid, V);
+        const uint4* zv = reinterpret_cast<const uint4*>(z + S.head);
+        uint4* dv = reinterpret_cast<uint4*>(dz + S.head);
+        const bool wide = reinterpret_cast<uintptr_t>(dz + S.head) % 16 == 0;
+        const float w_next = weight(row + step);
+        const auto put = [&](int i, const float (&x)[N]) {
+            if (wide) {
+                dv[i] = Vec<X>::put(x);
+            } else {
+#pragma unroll
+                for (int k = 0; k < N; ++k) from_f32(x[k], dz[S.head + (int64_t)i * N + k]);
+            }
+        };
+        // vectors of this thread behind those that are kept: four at a time
+        const auto stream = [&](auto f) {
+            for (int i = keep * DATA + tid; i < S.body; i += 4 * DATA) {
+                uint4 v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    v[u] = i + u * DATA < S.body ? zv[i + u * DATA] : Vec<X>::fill_low();
+                f(i, v);
+            }
+        };
+
+        if (w == 0.f) {
+            prefetch(row + step, w_next);
+            bar_sync(kListReady + b, ALL);
+            if (tid == 0) loss[row] = 0.f, lse[row] = 0.f;
+            if (GRAD) {
+                float zero[N] = {};
+                if (extra >= 0) from_f32(0.f, dz[extra]);
+                for (int i = tid; i < S.body; i += DATA) put(i, zero);
+            }
+        } else {
+            // this thread's maximum m and sum of 2^(c (z - m)); without a finite element: 0 or NaN
+            const float zx = extra >= 0 ? to_f32(z[extra]) : kNegInf;
+            float m = kNegInf, s = 0.f;
+            const auto add = [&](const uint4* v, int count) {
+                uint4 top = v[0];
+#pragma unroll
+                for (int u = 1; u < 4; ++u)
+                    if (u < count) top = Vec<X>::top(top, v[u]);
+                float f[N], a = m;
+                Vec<X>::get(top, f);
+#pragma unroll
+                for (int k = 0; k < N; ++k) a = fmaxf(a, f[k]);
+                if (a > m) s = m == kNegInf ? s : s * ex2((m - a) * c), m = a;
+                const float ref = m == kNegInf ? 0.f : m;
+                float part[2] = {0.f, 0.f};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (u >= count) break;
+                    Vec<X>::get(v[u], f);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) part[k % 2] += ex2((f[k] - ref) * c);
+                }
+                s += part[0] + part[1];
+            };
+            stream([&](int, const uint4 (&v)[4]) { add(v, 4); });
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            for (int u = 0; u < keep && u * DATA + tid < S.body; u += 4) {
+                uint4 v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    v[q] = u + q < keep && (u + q) * DATA + tid < S.body ? slot[(u + q) * DATA]
+                                                                        : Vec<X>::fill_low();
+                add(v, 4);
+            }
+            if (extra >= 0) join(m, s, zx, zx == kNegInf ? 0.f : ex2((zx - zx) * c), c);
+            const float mw = warp_max(m);
+            if (m != kNegInf) s *= ex2((m - mw) * c);
+            s = warp_sum(s);
+            if (lane == 0) pairs[b][tid / 32] = make_float2(mw, s);
+            if (!GRAD) prefetch(row + step, w_next);
+            bar_sync(kData, DATA);
+            join_pairs(pairs[b], DATA / 32, c, m, s);
+            bar_sync(kListReady + b, ALL);
+            const List L = list(b);
+            if (tid < 32) {
+                const float l = logf(s), kl = list_loss(T, L, m, l);
+                if (tid == 0) loss[row] = w * kl, lse[row] = m * T.inv_tau + l;
+            }
+            if (GRAD) {
+                const float f = w * T.inv_tau, mass = *L.mass;
+                const bool none = mass == 0.f;
+                const float fq = none ? 0.f : f * mass / s;
+                const auto grad = [&](float x) { return none ? 0.f : fq * ex2((x - m) * c); };
+                const auto write = [&](int i, const uint4& v) {
+                    float x[N];
+                    Vec<X>::get(v, x);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) x[k] = grad(x[k]);
+                    put(i, x);
+                };
+#pragma unroll 2
+                for (int u = 0; u < keep; ++u) {
+                    const int i = u * DATA + tid;
+                    if (i >= S.body) break;
+                    write(i, slot[u * DATA]);
+                }
+                prefetch(row + step, w_next);
+                stream([&](int i, const uint4 (&v)[4]) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (i + u * DATA < S.body) write(i + u * DATA, v[u]);
+                });
+                if (extra >= 0) from_f32(grad(zx), dz[extra]);
+                bar_sync(kData, DATA);
+                if (!none)
+                    for (int j = tid; j < T.k; j += DATA)
+                        if (L.at[j] >= 0)
+                            from_f32(fq * ex2((L.zt[j] - m) * c) - f * list_p(T, L, j),
+                                     dz[L.at[j]]);
+            }
+        }
+        if (row + 2 * (int64_t)step < rows) bar_arrive(kListFree + b, ALL);
+        w = w_next;
     }
 }
 
@@ -337,6 +576,26 @@ int launch(const X* z, int rows, int V, int64_t ld, const Teacher& T, float* los
     return cuda_err(e);
 }
 
+template <class X, int DATA>
+int launch_rows(const X* z, int rows, int V, int64_t ld, const Teacher& T, float* loss, float* lse,
+                X* dz, int64_t ldd, int* status, int sms, cudaStream_t st) {
+    constexpr int blocks = 1024 / DATA;         // of an SM
+    const size_t lists = (size_t)32 * ((T.k + 3) / 4 * 4) + (T.k > 32 ? kHash * 4 : 0);
+    const size_t room = 226 * 1024 / blocks - 1024 - 512;    // reserved, and the static arrays
+    const size_t vec = (size_t)DATA * 16;
+    size_t keep = room > lists ? (room - lists) / vec : 0;
+    keep = std::min(keep, ((size_t)V / Vec<X>::N + DATA - 1) / DATA);
+    const size_t smem = keep * vec + lists;
+    auto kern = dz ? distill_rows_kernel<X, DATA, true> : distill_rows_kernel<X, DATA, false>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+        cudaSuccess)
+        return BAKRON_ERR_CUDA;
+    kern<<<std::min(rows, blocks * sms), DATA + 32, smem, st>>>(z, rows, V, ld, T, loss, lse, dz, ldd,
+                                                                status, (int)keep);
+    count_launches(1);
+    return cuda_err(cudaGetLastError());
+}
+
 template <int D>
 int plan(const void* z_, int rows, int V, int64_t ld, const Teacher& T, float* loss, float* lse,
          void* dz_, int64_t ldd, int* status, cudaStream_t st) {
@@ -345,7 +604,13 @@ int plan(const void* z_, int rows, int V, int64_t ld, const Teacher& T, float* l
     X* dz = static_cast<X*>(dz_);
     const int sms = tc::sm_count();
     if (sms <= 0) return BAKRON_ERR_CUDA;
-    // Blocks a row: as many as keep its slices within 8 vectors a thread, and for few rows as
+    // Many rows: two blocks of 512 threads an SM, or eight of 128 where their kept vectors hold a row.
+    if (rows >= 2 * sms) {
+        if ((size_t)V * sizeof(X) <= 20 * 1024 && T.k <= 128)
+            return launch_rows<X, 128>(z, rows, V, ld, T, loss, lse, dz, ldd, status, sms, st);
+        return launch_rows<X, 512>(z, rows, V, ld, T, loss, lse, dz, ldd, status, sms, st);
+    }
+    // Few rows. Blocks a row: as many as keep its slices within 8 vectors a thread, and for few rows as
     // many as fill it (four blocks an SM), as long as a slice has a vector for every thread.
     const int vecs = V / Vec<X>::N;
     int ck = 1;
