@@ -310,3 +310,65 @@ def test_a_rounded_head_against_the_original(bk):
     want = dz.double() @ solver.W.double()
     a = dz.double().abs() @ solver.W.double().abs()
     assert ((dx.double() - want).abs() <= a * 30 * 2.0 ** -23).all()
+
+
+# rows enough that blocks go from row to row (two an SM and more), with rows that shared memory holds
+# whole, in part, and hardly at all
+@pytest.mark.parametrize("dt,V,k", [("f32", 5, 3), ("f16", 257, 40), ("bf16", 8000, 32),
+                                    ("bf16", 10241, 130), ("f32", 9001, 7), ("f16", 50001, 64),
+                                    ("bf16", 70000, 33), ("bf16", 131072, 64),
+                                    ("f32", 70003, 1024), ("f32", 140000, 9)])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_blocks_that_go_from_row_to_row(bk, dt, V, k, ragged):
+    """Every row of many against the same rows in small batches (which other kernels take), and a few
+    against the oracle."""
+    rows = 901 if V < 60000 else 605
+    z, idx, top, _ = _problem(rows, V, k, dt, V + k, repeat=ragged and k > 2)
+    w = None
+    if ragged:
+        gen = torch.Generator(device="cuda").manual_seed(V)
+        w = (torch.rand(rows, generator=gen, device="cuda") < 0.6).float() * 1.5
+        idx = torch.where(torch.rand(idx.shape, generator=gen, device="cuda") < 0.8, idx, -1)
+        if V > 100:
+            z[:, V // 2:V // 2 + 7] = -float("inf")
+    st = bk.new_status("cuda")
+    full = bk.distill(z, idx, top, 1.5, None, w, status=st)
+    alone = bk.distill(z, idx, top, 1.5, None, w, grad=False, status=st)
+    assert torch.equal(full[0].isinf(), alone[0].isinf()) and torch.equal(full[1], alone[1])
+    assert torch.equal(full[0], alone[0])
+    tol = 2 * ((V / 512 + 40) * 2.0 ** -24 + 2.0 ** -20)
+    for lo in range(0, rows, 64):
+        hi = min(rows, lo + 64)
+        part = bk.distill(z[lo:hi], idx[lo:hi], top[lo:hi], 1.5, None,
+                          None if w is None else w[lo:hi], status=st)
+        fin = torch.isfinite(part[0])
+        assert torch.equal(fin, torch.isfinite(full[0][lo:hi]))
+        assert ((full[1][lo:hi] - part[1]).abs() <= tol * (1 + part[1].abs())).all()
+        assert ((full[0][lo:hi] - part[0]).abs()[fin] <= 40 * tol).all()
+        a, b = full[2][lo:hi].float(), part[2].float()
+        assert ((a - b).abs() <= 2 * HALF[dt] * (b.abs() + TINY[dt]) + 40 * tol * b.abs()
+                + 2.0 ** -22).all()
+    assert bk.bakron_read_status(st) == 0
+    if not ragged:
+        _check(bk, z[-2:], idx[-2:], top[-2:], 1.5, dt=dt)
+        zl = bk.distill(z, idx, top, 1.5, dlogits=z)[2]        # in place
+        assert torch.equal(zl, full[2])
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows", [3, 400])
+def test_rows_of_nothing_but_the_lowest_value(bk, dt, rows):
+    """A mask of the type's lowest value over a whole row leaves equal probabilities."""
+    V = 1000
+    z = torch.full((rows, V), torch.finfo(DT[dt]).min, device="cuda", dtype=DT[dt])
+    z[0] = torch.randn(V, device="cuda")
+    idx = torch.arange(4, device="cuda").repeat(rows, 1)
+    top = torch.zeros(rows, 4, device="cuda")
+    for tau in (0.5, 1.0, 3.0):
+        loss, lse, dz = bk.distill(z, idx, top, tau)
+        want = np.log(0.25) + np.log(V)
+        if torch.finfo(DT[dt]).min / tau > -3.4e38:
+            assert (loss[1:] - want).abs().max() <= 1e-5
+        assert ((dz[1:, 4:].float() - 1 / V / tau).abs() <= 2 * HALF[dt] / V / tau + 1e-9).all()
+        assert ((dz[1:, :4].float() - (1 / V - 0.25) / tau).abs() <= 2 * HALF[dt] / tau).all()
+        assert torch.isfinite(loss[0]) and torch.isfinite(dz[0]).all()

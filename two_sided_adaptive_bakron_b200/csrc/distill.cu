@@ -13,12 +13,14 @@
 //     L2 for the gradient. One warp goes through the teacher's lists a row ahead. The barriers are
 //     named ones: between the data warps, and between them and the list's warp.
 //   * Few rows (distill_kernel): a row is shared by a cluster of up to 8 blocks, so that the rows fill
-//     the GPU; each block keeps its slice in registers (rows above 512 KB are streamed twice). The
+//     the GPU; each block keeps its slice in registers (rows above 256 KB are streamed twice). The
 //     blocks exchange (maximum, sum) pairs of their warps through distributed shared memory and join
 //     them in a fixed order.
 //
-// All statistics are fp32. Differences from a maximum are taken before they are scaled by 1 / tau, so
-// that nothing large cancels in log p - log q; exponentials are ex2.approx (2 units in the last place).
+// All statistics are fp32. With c = log2(e) / tau and R the rounded c m of a maximum m, an exponent is
+// c z - R in one rounding (fma): what R's rounding and c's are off cancels between a logit and the
+// sum it is divided by, so nothing large is lost in log p - log q. ex2.approx is good to 2 units in
+// the last place.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -35,8 +37,7 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxK = 1024;
-constexpr int kHash = 2 * kMaxK;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -INFINITY;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -45,16 +46,43 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Joins the pairs (m, s) and (m2, s2) that stand for s 2^(c m) and s2 2^(c m2).
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float c) {
-    const float top = fmaxf(m, m2);
-    if (top == kNegInf) {           // two empty parts (or NaN)
-        s += s2;
-        return;
+// What exponents are taken against: R = fl(c m) of a maximum m (0 where nothing is finite). Where R is
+// large, as with masks of the type's lowest value, its rounding is too, and differences from m are
+// taken first instead.
+struct Ref {
+    float m, R, c;
+    static __device__ __forceinline__ Ref of(float m, float c) {
+        return Ref{m, m == kNegInf ? 0.f : __fmul_rn(m, c), c};
     }
-    s = s * ex2((m - top) * c) + s2 * ex2((m2 - top) * c);
-    m = top;
-}
+    __device__ __forceinline__ bool usual() const { return fabsf(R) < 65536.f; }
+    // 2^(c (x - m))
+    __device__ __forceinline__ float term(float x) const {
+        return usual() ? ex2(fmaf(x, c, -R)) : ex2((x - m) * c);
+    }
+    template <int N>
+    __device__ __forceinline__ void terms(float (&x)[N]) const {
+        if (usual()) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) x[k] = ex2(fmaf(x[k], c, -R));
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) x[k] = ex2((x[k] - m) * c);
+        }
+    }
+    // the factor that brings a sum taken against m2 here; a sum without a finite element (0 or
+    // NaN) stays what it is
+    __device__ __forceinline__ float carry(float m2) const {
+        if (m2 == kNegInf) return 1.f;
+        const Ref o = of(m2, c);
+        return usual() ? ex2(o.usual() ? o.R - R : fmaf(m2, c, -R))
+                       : ex2(o.usual() ? fmaf(-m, c, o.R) : (m2 - m) * c);
+    }
+    // (x - m) / tau
+    __device__ __forceinline__ float scaled(float x) const {
+        return (usual() ? fmaf(x, c, -R) : (x - m) * c) * kLn2;
+    }
+    __device__ __forceinline__ float own(float inv_tau) const { return usual() ? R * kLn2 : m * inv_tau; }
+};
 
 struct Teacher {
     const void* idx; int idx64; const void* t; int td; int k;
@@ -87,41 +115,56 @@ __device__ __forceinline__ float warp_max(float v) {
 struct List {
     float *p, *lp, *zt; int *at, *seen; float* mass; int* twice;
 };
+// Slots of the table: a power of two, twice the list's length or more; none for short lists.
+__host__ __device__ inline int table_slots(int k) {
+    int n = 64;
+    while (n < 2 * k) n *= 2;
+    return k > 32 ? n : 0;
+}
 
 // A row's list, by one warp.
 template <class X>
 __device__ __forceinline__ void read_list(const Teacher& T, const X* z, int row, int V,
                                           const List& L, int* status) {
-    const int lane = threadIdx.x & 31;
-    if (T.k > 32) {
-        for (int e = lane; e < kHash; e += 32) L.seen[e] = -1;
-        __syncwarp();
-    }
+    const int lane = threadIdx.x & 31, slots = table_slots(T.k);
+    for (int e = lane; e < slots; e += 32) L.seen[e] = -1;
+    __syncwarp();
     float tmax = kNegInf;
     bool dup = false;
-    for (int j = lane; j < (T.k + 31) / 32 * 32; j += 32) {
-        int here = -1;
-        if (j < T.k) {
-            const size_t e = (size_t)row * T.k + j;
-            const long long i = index_at(T, e);
-            const float t = logit_at(T, e);
-            if (i >= V) set_status(status, BAKRON_ERR_INVALID_ARG);
-            const bool there = i >= 0 && i < V && t != kNegInf;
-            here = there ? (int)i : -1;
-            L.lp[j] = t;
-            L.zt[j] = there ? to_f32(z[i]) : 0.f;
-            if (there) tmax = fmaxf(tmax, t);
+    // four entries a lane at once: their loads, then the loads that these lead to
+    for (int j0 = lane; j0 - lane < T.k; j0 += 128) {
+        int here[4];
+        float t[4], x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = j0 + 32 * u;
+            here[u] = -1, t[u] = kNegInf;
+            if (j < T.k) {
+                const size_t e = (size_t)row * T.k + j;
+                const long long i = index_at(T, e);
+                t[u] = logit_at(T, e);
+                if (i >= V) set_status(status, BAKRON_ERR_INVALID_ARG);
+                if (i >= 0 && i < V && t[u] != kNegInf) here[u] = (int)i;
+            }
         }
-        if (j < (T.k + 3) / 4 * 4) L.at[j] = here;
-        if (T.k <= 32) {
-            const unsigned same = __match_any_sync(0xffffffffu, here);    // by every lane
-            dup = here >= 0 && __popc(same) > 1;
-        } else if (here >= 0) {
-            unsigned h = (unsigned)here * 2654435761u >> 21;
-            for (int step = 0; step < kHash; ++step, h = (h + 1) % kHash) {
-                const int was = atomicCAS(&L.seen[h], -1, here);
-                dup |= was == here;
-                if (was == -1 || was == here) break;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = here[u] >= 0 ? to_f32(z[here[u]]) : 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = j0 + 32 * u;
+            if (j < T.k) L.lp[j] = t[u], L.zt[j] = x[u];
+            if (j < (T.k + 3) / 4 * 4) L.at[j] = here[u];
+            if (here[u] >= 0) tmax = fmaxf(tmax, t[u]);
+            if (T.k <= 32) {
+                const unsigned same = __match_any_sync(0xffffffffu, here[u]);   // by every lane
+                dup |= here[u] >= 0 && __popc(same) > 1;
+            } else if (here[u] >= 0) {
+                unsigned h = ((unsigned)here[u] * 2654435761u >> 16) & (slots - 1);
+                for (int step = 0; step < slots; ++step, h = (h + 1) & (slots - 1)) {
+                    const int was = atomicCAS(&L.seen[h], -1, here[u]);
+                    dup |= was == here[u];
+                    if (was == -1 || was == here[u]) break;
+                }
             }
         }
     }
@@ -152,11 +195,11 @@ __device__ __forceinline__ void read_list(const Teacher& T, const X* z, int row,
     if (lane == 0) *L.mass = mass, *L.twice = dup;
 }
 
-// The loss of a row, by one warp, from the list and the row's (m, s).
-__device__ __forceinline__ float list_loss(const Teacher& T, const List& L, float m, float l) {
+// The loss of a row, by one warp: log q = (z - m) / tau - l.
+__device__ __forceinline__ float list_loss(const Teacher& T, const List& L, const Ref& ref, float l) {
     float kl = 0.f;
     for (int j = threadIdx.x & 31; j < T.k; j += 32)
-        if (L.p[j] != 0.f) kl += L.p[j] * (L.lp[j] - ((L.zt[j] - m) * T.inv_tau - l));
+        if (L.p[j] != 0.f) kl += L.p[j] * (L.lp[j] - (ref.scaled(L.zt[j]) - l));
     return warp_sum(kl);
 }
 
@@ -175,21 +218,18 @@ __device__ __forceinline__ float list_p(const Teacher& T, const List& L, int j) 
     return pj;
 }
 
-// Joins the pairs of a block's or cluster's warps, every warp for itself and all alike.
-__device__ __forceinline__ void join_pairs(const float2* pairs, int count, float c, float& m,
-                                           float& s) {
+// Joins the (maximum, sum) pairs of a block's or cluster's warps, every warp for itself and all
+// alike.
+__device__ __forceinline__ Ref join_pairs(const float2* pairs, int count, float c, float& s) {
     const int lane = threadIdx.x & 31;
-    m = kNegInf, s = 0.f;
-    for (int k = lane; k < count; k += 32) join(m, s, pairs[k].x, pairs[k].y, c);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        // both lanes of a pair join in the same order
-        float m1 = m, s1 = s, m2 = __shfl_xor_sync(0xffffffffu, m, o),
-              s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane & o) join(m2, s2, m1, s1, c), m = m2, s = s2;
-        else join(m1, s1, m2, s2, c), m = m1, s = s1;
-    }
-    if (fabsf(m) == INFINITY) s = NAN;      // +inf, or nothing but -inf
+    float m = kNegInf;
+    for (int k = lane; k < count; k += 32) m = fmaxf(m, pairs[k].x);
+    const Ref ref = Ref::of(warp_max(m), c);
+    s = 0.f;
+    for (int k = lane; k < count; k += 32) s += pairs[k].y * ref.carry(pairs[k].x);
+    s = warp_sum(s);
+    if (fabsf(ref.m) == INFINITY) s = NAN;      // +inf, or nothing but -inf
+    return ref;
 }
 
 // How a row lies to 16-byte boundaries: `head` elements, `body` vectors, `rest` elements.
@@ -208,13 +248,13 @@ template <class X> struct Span {
 
 // NV: 16-byte vectors that a thread holds (LOOP: of one round of the stream).
 template <class X, int NV, bool LOOP>
-__global__ void __launch_bounds__(kThreads, NV > 8 ? 2 : 4)
+__global__ void __launch_bounds__(kThreads, 4)
 distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict__ loss,
                float* __restrict__ lse, X* dz, int64_t ldd, int* __restrict__ status) {
     constexpr int N = Vec<X>::N;
     __shared__ float mass_of_list;
     __shared__ int twice;
-    __shared__ int seen[kHash];
+    __shared__ int seen[2 * kMaxK];
     __shared__ float2 pairs[8 * kWarps];              // (maximum, sum) of the cluster's warps
     __shared__ float p[kMaxK], lp[kMaxK], zt[kMaxK];
     __shared__ __align__(16) int at[kMaxK];
@@ -272,43 +312,46 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
     if (list && tid >= kThreads - 32)
         read_list<X>(T, z, row, V, L, status);
 
-    // the slice's maximum and sum of 2^(c (z - maximum)), warp by warp
+    // the slice's maximum and sum, warp by warp
     const float c = T.inv_tau * kLog2e;
     float m = zx, s = 0.f;
     auto thread_max = [&] {
         uint4 b = Vec<X>::fill_low();
 #pragma unroll
         for (int u = 0; u < NV; ++u) b = Vec<X>::top(b, v[u]);
-        float f[N], a = kNegInf;
-        Vec<X>::get(b, f);
-#pragma unroll
-        for (int k = 0; k < N; ++k) a = fmaxf(a, f[k]);
-        return a;
+        return Vec<X>::most(b);
     };
-    // a warp whose elements are all -inf (or NaN) counts its differences from 0
-    auto thread_sum = [&](float top) {
-        const float ref = top == kNegInf ? 0.f : top;
+    auto thread_sum = [&](const Ref& ref, int base) {
         float part[4] = {0.f, 0.f, 0.f, 0.f};
+        if (ref.usual()) {
 #pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            float f[N];
-            Vec<X>::get(v[u], f);
+            for (int u = 0; u < NV; ++u) {
+                float f[N];
+                Vec<X>::get(v[u], f);
 #pragma unroll
-            for (int k = 0; k < N; ++k) part[k % 4] += ex2((f[k] - ref) * c);
+                for (int k = 0; k < N; ++k) part[k % 4] += ex2(fmaf(f[k], c, -ref.R));
+            }
+        } else {        // from memory again: no second copy of the loop over the registers
+            for (int i = base + tid; i < min(v1, base + NV * kThreads); i += kThreads) {
+                float f[N];
+                Vec<X>::get(zv[i], f);
+#pragma unroll
+                for (int k = 0; k < N; ++k) part[0] += ex2((f[k] - ref.m) * c);
+            }
         }
         return (part[0] + part[1]) + (part[2] + part[3]);
     };
     if constexpr (!LOOP) {
         m = warp_max(fmaxf(m, thread_max()));
-        s = thread_sum(m);
-        if (extra >= 0) s += ex2((zx - (m == kNegInf ? 0.f : m)) * c);
+        s = thread_sum(Ref::of(m, c), v0);
+        if (extra >= 0) s += Ref::of(m, c).term(zx);
     } else {
         m = warp_max(m);
-        if (extra >= 0) s = ex2((zx - (m == kNegInf ? 0.f : m)) * c);
+        if (extra >= 0) s = Ref::of(m, c).term(zx);
         for (int base = v0;;) {
             const float top = fmaxf(m, warp_max(thread_max()));
-            if (top > m) s = m == kNegInf ? s : s * ex2((m - top) * c), m = top;
-            s += thread_sum(m);
+            if (top > m) s *= Ref::of(top, c).carry(m), m = top;
+            s += thread_sum(Ref::of(m, c), base);
             base += NV * kThreads;
             if (base >= v1) break;
             load(base);
@@ -324,11 +367,11 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
         if ((tid & 31) == 0) pairs[tid / 32] = make_float2(m, s);
         __syncthreads();
     }
-    join_pairs(pairs, ck * kWarps, c, m, s);
+    const Ref ref = join_pairs(pairs, ck * kWarps, c, s);
     if (rank == 0 && tid >= kThreads - 32) {
         const float l = logf(s);
-        const float kl = list_loss(T, L, m, l);
-        if (lane == 0) loss[row] = w * kl, lse[row] = m * T.inv_tau + l;
+        const float kl = list_loss(T, L, ref, l);
+        if (lane == 0) loss[row] = w * kl, lse[row] = ref.own(T.inv_tau) + l;
     }
     if (!dz) return;
 
@@ -340,23 +383,35 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
     const float f = w * T.inv_tau, mass = mass_of_list;
     const bool none = mass == 0.f;
     const float fq = none ? 0.f : f * mass / s;
-    auto grad = [&](float x) { return none ? 0.f : fq * ex2((x - m) * c); };
-    if (extra >= 0) from_f32(grad(zx), dz[extra]);
-    for (int base = v0; base < v1; base += NV * kThreads) {
-        if (LOOP) load(base);
+    if (extra >= 0) from_f32(none ? 0.f : fq * ref.term(zx), dz[extra]);
+    const auto put = [&](int i, const float (&x)[N]) {
+        if (wide) {
+            reinterpret_cast<uint4*>(dz + head)[i] = Vec<X>::put(x);
+        } else {
 #pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            const int i = base + u * kThreads + tid;
-            if (i >= v1) break;
+            for (int k = 0; k < N; ++k) from_f32(x[k], dz[head + (int64_t)i * N + k]);
+        }
+    };
+    if (none || !ref.usual()) {
+        for (int i = v0 + tid; i < v1; i += kThreads) {
             float x[N];
-            Vec<X>::get(v[u], x);
+            Vec<X>::get(zv[i], x);
 #pragma unroll
-            for (int k = 0; k < N; ++k) x[k] = grad(x[k]);
-            if (wide) {
-                reinterpret_cast<uint4*>(dz + head)[i] = Vec<X>::put(x);
-            } else {
+            for (int k = 0; k < N; ++k) x[k] = none ? 0.f : fq * ex2((x[k] - ref.m) * c);
+            put(i, x);
+        }
+    } else {
+        for (int base = v0; base < v1; base += NV * kThreads) {
+            if (LOOP) load(base);
 #pragma unroll
-                for (int k = 0; k < N; ++k) from_f32(x[k], dz[head + (int64_t)i * N + k]);
+            for (int u = 0; u < NV; ++u) {
+                const int i = base + u * kThreads + tid;
+                if (i >= v1) break;
+                float x[N];
+                Vec<X>::get(v[u], x);
+#pragma unroll
+                for (int k = 0; k < N; ++k) x[k] = fq * ex2(fmaf(x[k], c, -ref.R));
+                put(i, x);
             }
         }
     }
@@ -367,7 +422,7 @@ distill_kernel(const X* z, int V, int64_t ld, const Teacher T, float* __restrict
         if (i < 0) continue;
         const int vec = i < head || i >= V - rest ? -1 : (i - head) / N;
         if (vec < 0 ? rank != 0 : vec < v0 || vec >= v1) continue;
-        from_f32(fq * ex2((zt[j] - m) * c) - f * list_p(T, L, j), dz[i]);
+        from_f32(fq * ref.term(zt[j]) - f * list_p(T, L, j), dz[i]);
     }
 }
 
@@ -379,13 +434,14 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) {
 }
 
 // Blocks that go from row to row: DATA threads and a warp for the lists. `keep`: vectors of a row
-// that a thread keeps in shared memory.
+// that a thread keeps in shared memory; the next kRegs are kept in registers, others are streamed.
 template <class X, int DATA, bool GRAD>
 __global__ void __launch_bounds__(DATA + 32, 1024 / DATA)
 distill_rows_kernel(const X* z0, int rows, int V, int64_t ld, const Teacher T,
                     float* __restrict__ loss, float* __restrict__ lse, X* dz0, int64_t ldd,
                     int* __restrict__ status, int keep) {
     constexpr int N = Vec<X>::N, ALL = DATA + 32;
+    constexpr int kRegs = DATA == 992 ? 4 : 1;
     enum { kData = 1, kListReady = 2, kListFree = 4 };      // barriers (the last two: one a buffer)
     extern __shared__ __align__(16) char smem[];
     __shared__ float2 pairs[2][DATA / 32];
@@ -415,44 +471,82 @@ distill_rows_kernel(const X* z0, int rows, int V, int64_t ld, const Teacher T,
     uint4* slot = reinterpret_cast<uint4*>(smem) + tid;
     const uint32_t slot32 = (uint32_t)__cvta_generic_to_shared(slot);
     const auto weight = [&](int row) { return row < rows ? T.w ? T.w[row] : 1.f : 0.f; };
-    // starts the copies of the vectors that are kept of a row
-    const auto prefetch = [&](int row, float w) {
-        if (w != 0.f) {
-            const X* z = z0 + (int64_t)row * ld;
-            const Span<X> S(z, V);
-            const uint4* zv = reinterpret_cast<const uint4*>(z + S.head) + tid;
-            for (int u = 0; u < keep && u * DATA + tid < S.body; ++u)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot32 +
-                                                                               u * DATA * 16),
-                             "l"(zv + u * DATA)
+    // copies of the vectors that are kept of the row to come, slot by slot
+    // Rows that are whole vectors apart lie alike to the boundaries.
+    struct Next { const uint4* v; int body; };
+    const bool alike = ld * (int64_t)sizeof(X) % 16 == 0;
+    const Span<X> S0(z0, V);
+    const auto next_row = [&](const X* z, float w) {
+        const Span<X> S = alike ? S0 : Span<X>(z, V);
+        return Next{reinterpret_cast<const uint4*>(z + S.head) + tid, w != 0.f ? S.body : 0};
+    };
+    const auto copy = [&](const Next& nx, int u) {
+        if (u * DATA + tid < nx.body)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot32 + u * DATA * 16),
+                         "l"(nx.v + u * DATA)
+                         : "memory");
+    };
+    // They are made and waited for in groups of four slots, `groups` a row (empty ones included), so
+    // that what is pending can be counted.
+    const int groups = (keep + 3) / 4;
+    unsigned long long once;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+    const auto copy_group = [&](const Next& nx, int q) {
+        if (4 * q + 4 <= keep && (4 * q + 4) * DATA <= nx.body) {
+            const uint4* src = nx.v + 4 * q * DATA;
+            const uint32_t dst = slot32 + 4 * q * DATA * 16;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst + u * DATA * 16),
+                             "l"(src + u * DATA), "l"(once)
                              : "memory");
+        } else {
+            for (int u = 4 * q; u < min(4 * q + 4, keep); ++u) copy(nx, u);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    const auto wait = [](int pending) {
+        switch (pending) {
+            case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+            case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+            case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+            default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        }
+    };
 
     float w = weight(blockIdx.x);
-    prefetch(blockIdx.x, w);
+    const X* z = z0 + (int64_t)blockIdx.x * ld;
+    X* dz = GRAD ? dz0 + (int64_t)blockIdx.x * ldd : nullptr;
+    {
+        const Next first_row = next_row(z, w);
+        for (int q = 0; q < groups; ++q) copy_group(first_row, q);
+    }
     for (int row = blockIdx.x, it = 0; row < rows; row += step, ++it) {
         const int b = it & 1;
-        const X* z = z0 + (int64_t)row * ld;
-        X* dz = GRAD ? dz0 + (int64_t)row * ldd : nullptr;
-        const Span<X> S(z, V);
+        const Span<X> S = alike ? S0 : Span<X>(z, V);
         const int extra = S.extra(tid, V);
         const uint4* zv = reinterpret_cast<const uint4*>(z + S.head);
         uint4* dv = reinterpret_cast<uint4*>(dz + S.head);
         const bool wide = reinterpret_cast<uintptr_t>(dz + S.head) % 16 == 0;
         const float w_next = weight(row + step);
+        const Next next = next_row(z + (int64_t)step * ld, w_next);
         const auto put = [&](int i, const float (&x)[N]) {
             if (wide) {
-                dv[i] = Vec<X>::put(x);
+                __stcs(dv + i, Vec<X>::put(x));
             } else {
 #pragma unroll
                 for (int k = 0; k < N; ++k) from_f32(x[k], dz[S.head + (int64_t)i * N + k]);
             }
         };
-        // vectors of this thread behind those that are kept: four at a time
+        const auto put_zeros = [&] {
+            const float zero[N] = {};
+            if (extra >= 0) from_f32(0.f, dz[extra]);
+            for (int i = tid; i < S.body; i += DATA) put(i, zero);
+        };
+        // vectors of this thread behind those that are kept: a few at a time
+        const int first = (keep + kRegs) * DATA + tid;
         const auto stream = [&](auto f) {
-            for (int i = keep * DATA + tid; i < S.body; i += 4 * DATA) {
+            for (int i = first; i < S.body; i += 4 * DATA) {
                 uint4 v[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
@@ -462,98 +556,131 @@ distill_rows_kernel(const X* z0, int rows, int V, int64_t ld, const Teacher T,
         };
 
         if (w == 0.f) {
-            prefetch(row + step, w_next);
+            for (int q = 0; q < groups; ++q) copy_group(next, q);
             bar_sync(kListReady + b, ALL);
             if (tid == 0) loss[row] = 0.f, lse[row] = 0.f;
-            if (GRAD) {
-                float zero[N] = {};
-                if (extra >= 0) from_f32(0.f, dz[extra]);
-                for (int i = tid; i < S.body; i += DATA) put(i, zero);
-            }
+            if (GRAD) put_zeros();
         } else {
-            // this thread's maximum m and sum of 2^(c (z - m)); without a finite element: 0 or NaN
+            // this thread's maximum m and sum
             const float zx = extra >= 0 ? to_f32(z[extra]) : kNegInf;
             float m = kNegInf, s = 0.f;
-            const auto add = [&](const uint4* v, int count) {
+            const auto add = [&](const auto& v) {
+                constexpr int count = sizeof(v) / sizeof(uint4);
                 uint4 top = v[0];
 #pragma unroll
-                for (int u = 1; u < 4; ++u)
-                    if (u < count) top = Vec<X>::top(top, v[u]);
-                float f[N], a = m;
-                Vec<X>::get(top, f);
-#pragma unroll
-                for (int k = 0; k < N; ++k) a = fmaxf(a, f[k]);
-                if (a > m) s = m == kNegInf ? s : s * ex2((m - a) * c), m = a;
-                const float ref = m == kNegInf ? 0.f : m;
+                for (int u = 1; u < count; ++u) top = Vec<X>::top(top, v[u]);
+                const float a = fmaxf(m, Vec<X>::most(top));
+                float f[N];
+                if (a > m) s *= Ref::of(a, c).carry(m), m = a;
+                const Ref own = Ref::of(m, c);
                 float part[2] = {0.f, 0.f};
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (u >= count) break;
+                for (int u = 0; u < count; ++u) {
                     Vec<X>::get(v[u], f);
+                    own.terms(f);
 #pragma unroll
-                    for (int k = 0; k < N; ++k) part[k % 2] += ex2((f[k] - ref) * c);
+                    for (int k = 0; k < N; ++k) part[k % 2] += f[k];
                 }
                 s += part[0] + part[1];
             };
-            stream([&](int, const uint4 (&v)[4]) { add(v, 4); });
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            for (int u = 0; u < keep && u * DATA + tid < S.body; u += 4) {
-                uint4 v[4];
+            uint4 held[kRegs];
+            const bool hold = keep * DATA < S.body;
+            if (hold) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    v[q] = u + q < keep && (u + q) * DATA + tid < S.body ? slot[(u + q) * DATA]
-                                                                        : Vec<X>::fill_low();
-                add(v, 4);
+                for (int u = 0; u < kRegs; ++u) {
+                    const int i = (keep + u) * DATA + tid;
+                    held[u] = i < S.body ? zv[i] : Vec<X>::fill_low();
+                }
             }
-            if (extra >= 0) join(m, s, zx, zx == kNegInf ? 0.f : ex2((zx - zx) * c), c);
-            const float mw = warp_max(m);
-            if (m != kNegInf) s *= ex2((m - mw) * c);
+            stream([&](int, const uint4 (&v)[4]) { add(v); });
+            for (int q = 0; q < groups; ++q) {
+                wait(GRAD ? groups - 1 - q : groups - 1);
+                uint4 v[4];
+                if (4 * q + 4 <= keep && (4 * q + 4) * DATA <= S.body) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = slot[(4 * q + k) * DATA];
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int u = 4 * q + k;
+                        v[k] = u < keep && u * DATA + tid < S.body ? slot[u * DATA]
+                                                                   : Vec<X>::fill_low();
+                    }
+                }
+                add(v);
+                if (!GRAD) copy_group(next, q);
+            }
+            if (hold) add(held);
+            const float mw = warp_max(fmaxf(m, zx));
+            s *= Ref::of(mw, c).carry(m);
+            if (extra >= 0) s += Ref::of(mw, c).term(zx);
             s = warp_sum(s);
             if (lane == 0) pairs[b][tid / 32] = make_float2(mw, s);
-            if (!GRAD) prefetch(row + step, w_next);
             bar_sync(kData, DATA);
-            join_pairs(pairs[b], DATA / 32, c, m, s);
+            const Ref ref = join_pairs(pairs[b], DATA / 32, c, s);
             bar_sync(kListReady + b, ALL);
             const List L = list(b);
             if (tid < 32) {
-                const float l = logf(s), kl = list_loss(T, L, m, l);
-                if (tid == 0) loss[row] = w * kl, lse[row] = m * T.inv_tau + l;
+                const float l = logf(s), kl = list_loss(T, L, ref, l);
+                if (tid == 0) loss[row] = w * kl, lse[row] = ref.own(T.inv_tau) + l;
             }
             if (GRAD) {
                 const float f = w * T.inv_tau, mass = *L.mass;
-                const bool none = mass == 0.f;
-                const float fq = none ? 0.f : f * mass / s;
-                const auto grad = [&](float x) { return none ? 0.f : fq * ex2((x - m) * c); };
+                const float fq = f * mass / s;
                 const auto write = [&](int i, const uint4& v) {
                     float x[N];
                     Vec<X>::get(v, x);
+                    ref.terms(x);
 #pragma unroll
-                    for (int k = 0; k < N; ++k) x[k] = grad(x[k]);
+                    for (int k = 0; k < N; ++k) x[k] *= fq;
                     put(i, x);
                 };
-#pragma unroll 2
-                for (int u = 0; u < keep; ++u) {
-                    const int i = u * DATA + tid;
-                    if (i >= S.body) break;
-                    write(i, slot[u * DATA]);
-                }
-                prefetch(row + step, w_next);
-                stream([&](int i, const uint4 (&v)[4]) {
+                const bool plain = wide && ref.usual() && mass != 0.f;
+                for (int q = 0; q < groups; ++q) {
+                    if (plain && 4 * q + 4 <= keep && (4 * q + 4) * DATA <= S.body) {
+                        const uint4* from = slot + 4 * q * DATA;
+                        uint4* to = dv + 4 * q * DATA + tid;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (i + u * DATA < S.body) write(i + u * DATA, v[u]);
-                });
-                if (extra >= 0) from_f32(grad(zx), dz[extra]);
-                bar_sync(kData, DATA);
-                if (!none)
+                        for (int u = 0; u < 4; ++u) {
+                            float x[N];
+                            Vec<X>::get(from[u * DATA], x);
+#pragma unroll
+                            for (int k = 0; k < N; ++k) x[k] = fq * ex2(fmaf(x[k], c, -ref.R));
+                            __stcs(to + u * DATA, Vec<X>::put(x));
+                        }
+                    } else if (mass != 0.f) {
+                        for (int u = 4 * q; u < min(4 * q + 4, keep); ++u)
+                            if (u * DATA + tid < S.body) write(u * DATA + tid, slot[u * DATA]);
+                    }
+                    copy_group(next, q);
+                }
+                if (mass != 0.f) {
+                    if (hold) {
+#pragma unroll
+                        for (int u = 0; u < kRegs; ++u) {
+                            const int i = (keep + u) * DATA + tid;
+                            if (i < S.body) write(i, held[u]);
+                        }
+                    }
+                    stream([&](int i, const uint4 (&v)[4]) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (i + u * DATA < S.body) write(i + u * DATA, v[u]);
+                    });
+                    if (extra >= 0) from_f32(fq * ref.term(zx), dz[extra]);
+                    bar_sync(kData, DATA);
                     for (int j = tid; j < T.k; j += DATA)
                         if (L.at[j] >= 0)
-                            from_f32(fq * ex2((L.zt[j] - m) * c) - f * list_p(T, L, j),
+                            from_f32(fq * ref.term(L.zt[j]) - f * list_p(T, L, j),
                                      dz[L.at[j]]);
+                } else {
+                    put_zeros();        // an empty list, whatever the logits are
+                }
             }
         }
         if (row + 2 * (int64_t)step < rows) bar_arrive(kListFree + b, ALL);
-        w = w_next;
+        w = w_next, z += (int64_t)step * ld;
+        if (GRAD) dz += (int64_t)step * ldd;
     }
 }
 
@@ -579,12 +706,12 @@ int launch(const X* z, int rows, int V, int64_t ld, const Teacher& T, float* los
 template <class X, int DATA>
 int launch_rows(const X* z, int rows, int V, int64_t ld, const Teacher& T, float* loss, float* lse,
                 X* dz, int64_t ldd, int* status, int sms, cudaStream_t st) {
-    constexpr int blocks = 1024 / DATA;         // of an SM
-    const size_t lists = (size_t)32 * ((T.k + 3) / 4 * 4) + (T.k > 32 ? kHash * 4 : 0);
+    constexpr int blocks = 1024 / DATA;         // of an SM (1 of 992)
+    const size_t lists = (size_t)32 * ((T.k + 3) / 4 * 4) + (size_t)table_slots(T.k) * 4;
     const size_t room = 226 * 1024 / blocks - 1024 - 512;    // reserved, and the static arrays
     const size_t vec = (size_t)DATA * 16;
     size_t keep = room > lists ? (room - lists) / vec : 0;
-    keep = std::min(keep, ((size_t)V / Vec<X>::N + DATA - 1) / DATA);
+    keep = std::min({keep, (size_t)16, ((size_t)V / Vec<X>::N + DATA - 1) / DATA});
     const size_t smem = keep * vec + lists;
     auto kern = dz ? distill_rows_kernel<X, DATA, true> : distill_rows_kernel<X, DATA, false>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
@@ -604,14 +731,20 @@ int plan(const void* z_, int rows, int V, int64_t ld, const Teacher& T, float* l
     X* dz = static_cast<X*>(dz_);
     const int sms = tc::sm_count();
     if (sms <= 0) return BAKRON_ERR_CUDA;
-    // Many rows: two blocks of 512 threads an SM, or eight of 128 where their kept vectors hold a row.
+    // Many rows: eight blocks of 128 threads an SM up to 24 KB a row, then two of 512, and one of 992
+    // above 384 KB, where two rows an SM would read most of themselves twice (measured with the
+    // gradient, 512 / 992 threads: 260 / 280 us for 2048 rows of 256 KB, 293 / 239 us for 1024 of
+    // 512 KB; four blocks of 256 for 64 KB took 76 us, two of 512 take 72).
     if (rows >= 2 * sms) {
-        if ((size_t)V * sizeof(X) <= 20 * 1024 && T.k <= 128)
+        const size_t row = (size_t)V * sizeof(X);
+        if (row <= 24 * 1024)
             return launch_rows<X, 128>(z, rows, V, ld, T, loss, lse, dz, ldd, status, sms, st);
-        return launch_rows<X, 512>(z, rows, V, ld, T, loss, lse, dz, ldd, status, sms, st);
+        if (row <= 384 * 1024)
+            return launch_rows<X, 512>(z, rows, V, ld, T, loss, lse, dz, ldd, status, sms, st);
+        return launch_rows<X, 992>(z, rows, V, ld, T, loss, lse, dz, ldd, status, sms, st);
     }
-    // Few rows. Blocks a row: as many as keep its slices within 8 vectors a thread, and for few rows as
-    // many as fill it (four blocks an SM), as long as a slice has a vector for every thread.
+    // Few rows. Blocks a row: as many as keep its slices within 8 vectors a thread or fill the GPU
+    // (four blocks an SM), as long as a slice has a vector for every thread.
     const int vecs = V / Vec<X>::N;
     int ck = 1;
     while (ck < 8 && vecs > ck * 8 * kThreads) ck *= 2;
@@ -623,8 +756,6 @@ int plan(const void* z_, int rows, int V, int64_t ld, const Teacher& T, float* l
     if (nv <= 2) return launch<X, 2, false>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
     if (nv <= 4) return launch<X, 4, false>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
     if (nv <= 8) return launch<X, 8, false>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
-    if (nv <= 16)
-        return launch<X, 16, false>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
     return launch<X, 4, true>(z, rows, V, ld, T, loss, lse, dz, ldd, status, ck, st);
 }
 

@@ -25,7 +25,8 @@ __device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
 __device__ __forceinline__ void from_f32(float v, __half& o) { o = __float2half_rn(v); }
 __device__ __forceinline__ void from_f32(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
 
-// The elements of 16 bytes as fp32 and back, and the larger ones of two vectors (NaN loses).
+// The elements of 16 bytes as fp32 and back, the larger ones of two vectors, the largest of one (NaN
+// loses).
 template <class X> struct Vec;
 template <> struct Vec<float> {
     static constexpr int N = 4;
@@ -42,6 +43,10 @@ template <> struct Vec<float> {
             return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y)));
         };
         return make_uint4(f(a.x, b.x), f(a.y, b.y), f(a.z, b.z), f(a.w, b.w));
+    }
+    static __device__ __forceinline__ float most(const uint4& a) {
+        return fmaxf(fmaxf(__uint_as_float(a.x), __uint_as_float(a.y)),
+                     fmaxf(__uint_as_float(a.z), __uint_as_float(a.w)));
     }
     static __device__ __forceinline__ uint4 fill_low() {
         return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
@@ -74,6 +79,11 @@ template <> struct Vec<__half> {
         };
         return make_uint4(f(a.x, b.x), f(a.y, b.y), f(a.z, b.z), f(a.w, b.w));
     }
+    static __device__ __forceinline__ float most(const uint4& a) {
+        const __half2 *p = reinterpret_cast<const __half2*>(&a);
+        const float2 f = __half22float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
+        return fmaxf(f.x, f.y);
+    }
     static __device__ __forceinline__ uint4 fill_low() {
         return make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u);
     }
@@ -104,6 +114,11 @@ template <> struct Vec<__nv_bfloat16> {
             return *reinterpret_cast<const uint32_t*>(&m);
         };
         return make_uint4(f(a.x, b.x), f(a.y, b.y), f(a.z, b.z), f(a.w, b.w));
+    }
+    static __device__ __forceinline__ float most(const uint4& a) {
+        const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162*>(&a);
+        const float2 f = __bfloat1622float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
+        return fmaxf(f.x, f.y);
     }
     static __device__ __forceinline__ uint4 fill_low() {
         return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
