@@ -57,7 +57,7 @@ constexpr int token_rows(int k) { return is_split(k) ? 3 : 1; }
 // pairs (64 to 96 KB) where there is one.
 constexpr int batch_of(int k) { return is_book(k) ? 4 : 8; }   // column tiles of a stage
 constexpr int warps_of(int k) { return is_book(k) ? 16 : 8; }
-constexpr int blocks_of(int k) { return is_book(k) ? 1 : 2; }
+constexpr int blocks_of(int k) { return 16 / warps_of(k); }
 
 struct Book { uint32_t part[3][16]; };   // 16-bit parts of the entries (host-made)
 
@@ -192,10 +192,9 @@ __device__ __forceinline__ void split3(float v, uint32_t (&h)[3]) {
 // Copies columns [j0, j0 + 64 tiles) of tokens [t0, t0 + count) to shared memory as the products
 // take them: 16-bit and 8-bit activations as they are (asynchronously where their rows are aligned),
 // int8 as f16 for a codebook, fp32 in its three parts. Columns from n on are zeros.
-template <int K, class X>
+template <int K, int kThreads, class X>
 __device__ __forceinline__ void stage_x(char* sx, const Args& a, int t0, int count, int j0,
                                         int tiles) {
-    constexpr int kThreads = warps_of(K) * 32;
     const X* x = static_cast<const X*>(a.x) + (int64_t)t0 * a.ldx;
     const bool wide = a.ldx * sizeof(X) % 16 == 0 &&
                       reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
@@ -288,16 +287,16 @@ matvec4_kernel(const __grid_constant__ Args a) {
     const int xg0 = a.Gx > 1 ? kt0 * 64 / a.gx : 0;
 
     if constexpr (K == kF32 || K == kF32Book) {
-        stage_x<K, float>(sx, a, t0, count, kt0 * 64, batches * kBatch);
+        stage_x<K, kThreads, float>(sx, a, t0, count, kt0 * 64, batches * kBatch);
     } else if constexpr (K == kF16) {
-        stage_x<K, __half>(sx, a, t0, count, kt0 * 64, batches * kBatch);
+        stage_x<K, kThreads, __half>(sx, a, t0, count, kt0 * 64, batches * kBatch);
     } else if constexpr (K == kI8) {
-        stage_x<K, int8_t>(sx, a, t0, count, kt0 * 64, batches * kBatch);
+        stage_x<K, kThreads, int8_t>(sx, a, t0, count, kt0 * 64, batches * kBatch);
     } else if constexpr (K == kF16Book) {
-        if (a.x_dtype == BAKRON_I8) stage_x<K, int8_t>(sx, a, t0, count, kt0 * 64, batches * kBatch);
-        else stage_x<K, __half>(sx, a, t0, count, kt0 * 64, batches * kBatch);
+        if (a.x_dtype == BAKRON_I8) stage_x<K, kThreads, int8_t>(sx, a, t0, count, kt0 * 64, batches * kBatch);
+        else stage_x<K, kThreads, __half>(sx, a, t0, count, kt0 * 64, batches * kBatch);
     } else {
-        stage_x<K, __nv_bfloat16>(sx, a, t0, count, kt0 * 64, batches * kBatch);
+        stage_x<K, kThreads, __nv_bfloat16>(sx, a, t0, count, kt0 * 64, batches * kBatch);
     }
     copy_commit();
 
@@ -352,13 +351,21 @@ matvec4_kernel(const __grid_constant__ Args a) {
     for (int k = 0; k < kStages - 1; ++k) fetch();
 
     if constexpr (is_book(K)) {
-        // entry e of a plane: codes e % 16 and e / 16, once for every lane
+        // entry b, codes b % 16 and b / 16, once for every lane: planes 0 and 1 of a lane side by
+        // side, plane 2 behind them
         uint4* dst = reinterpret_cast<uint4*>(const_cast<uint32_t*>(table));
-        for (int e = threadIdx.x; e < planes(K) * 256 * 8; e += kThreads) {
-            const int pl = e / 2048, b = e / 8 % 256;
-            const uint32_t v = a.book.part[pl][b % 16] | a.book.part[pl][b / 16] << 16;
-            dst[e] = make_uint4(v, v, v, v);
+        const auto pair = [&](int pl, int b) {
+            return a.book.part[pl][b % 16] | a.book.part[pl][b / 16] << 16;
+        };
+        for (int e = threadIdx.x; e < 4096; e += kThreads) {
+            const uint32_t u = pair(0, e / 16), v = pair(1, e / 16);
+            dst[e] = make_uint4(u, v, u, v);
         }
+        if constexpr (planes(K) == 3)
+            for (int e = threadIdx.x; e < 2048; e += kThreads) {
+                const uint32_t v = pair(2, e / 8);
+                dst[4096 + e] = make_uint4(v, v, v, v);
+            }
     }
     const int xgn = a.Gx > 1 ? (kt1 * 64 + a.gx - 1) / a.gx - xg0 : 0;   // steps of x in the slice
     if constexpr (K == kI8 || K == kF16Book) {
@@ -452,19 +459,35 @@ matvec4_kernel(const __grid_constant__ Args a) {
                         else
                             B[q] = v;
                     }
+                    uint2 e0[4], e1[4];      // codebook: planes 0 and 1
+                    if constexpr (is_book(K)) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            // byte * 256 + lane * 8
+                            const char* tb = reinterpret_cast<const char*>(table);
+                            e0[q] = *reinterpret_cast<const uint2*>(
+                                tb + __byte_perm(w0, 8 * lane, 0x5504 | q << 4));
+                            e1[q] = *reinterpret_cast<const uint2*>(
+                                tb + __byte_perm(w1, 8 * lane, 0x5504 | q << 4));
+                        }
+                    }
 #pragma unroll
                     for (int pl = 0; pl < (is_book(K) ? planes(K) : 1); ++pl) {
                         uint32_t p0[4], p1[4];
                         if constexpr (is_book(K)) {
-                            const char* tb = reinterpret_cast<const char*>(table) + pl * 32768;
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
-                                const uint32_t s0 = q == 0 ? w0 << 7 : w0 >> (8 * q - 7);
-                                const uint32_t s1 = q == 0 ? w1 << 7 : w1 >> (8 * q - 7);
-                                p0[q] = *reinterpret_cast<const uint32_t*>(
-                                    tb + ((s0 & 0x7F80u) | (4 * lane)));
-                                p1[q] = *reinterpret_cast<const uint32_t*>(
-                                    tb + ((s1 & 0x7F80u) | (4 * lane)));
+                                if (pl < 2) {
+                                    p0[q] = pl ? e0[q].y : e0[q].x;
+                                    p1[q] = pl ? e1[q].y : e1[q].x;
+                                } else {      // byte * 128 + lane * 4 of a table of its own
+                                    const char* tb =
+                                        reinterpret_cast<const char*>(table) + 65536 + 4 * lane;
+                                    p0[q] = *reinterpret_cast<const uint32_t*>(
+                                        tb + (w0 >> (8 * q) & 0xFF) * 128);
+                                    p1[q] = *reinterpret_cast<const uint32_t*>(
+                                        tb + (w1 >> (8 * q) & 0xFF) * 128);
+                                }
                             }
                         } else if constexpr (is_half(K)) {
                             codes_f16(w0, p0);
@@ -549,24 +572,37 @@ matvec4_kernel(const __grid_constant__ Args a) {
             part[(e / 16) * rows + tile * 16 + e % 16] += head[w * kTok * 16 + e];
     }
 
-    // the blocks of the cluster add up a share of the rows each
+    // the blocks of the cluster add up a share of the rows each, four rows a thread
     if (ck > 1) cluster.sync();
     else __syncthreads();
-    const int mine = (rt1 - rt0) * 16, share = (mine + ck - 1) / ck;
+    const int quads = (rt1 - rt0) * 4, share = (quads + ck - 1) / ck;
     for (int e = threadIdx.x; e < share * count; e += kThreads) {
-        const int tk = e / share, r = rank * share + e - tk * share;
-        const int64_t i = (int64_t)rt0 * 16 + r;
-        if (r >= mine || i >= a.m) continue;
-        float v = 0.f;
-        for (int c = 0; c < ck; ++c)
-            v += (ck > 1 ? cluster.map_shared_rank(part, c) : part)[tk * rows + r];
-        v = v * a.out1 * a.out2;
+        const int tk = e / share, quad = rank * share + e - tk * share;
+        const int64_t i = (int64_t)rt0 * 16 + 4 * quad;
+        if (quad >= quads || i >= a.m) continue;
+        float4 got[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < ck)
+                got[c] = *reinterpret_cast<const float4*>(
+                    (ck > 1 ? cluster.map_shared_rank(part, c) : part) + tk * rows + 4 * quad);
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < ck) v[0] += got[c].x, v[1] += got[c].y, v[2] += got[c].z, v[3] += got[c].w;
+        float f = 1.f;
         if (K == kI8 || K == kF16Book)
-            if (a.Gx == 1 && a.xs) v *= a.xs[t0 + tk];
+            if (a.Gx == 1 && a.xs) f = a.xs[t0 + tk];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = v[r] * a.out1 * a.out2 * f;
         const int64_t o = (int64_t)(t0 + tk) * a.ldy + i;
-        if (a.y_dtype == BAKRON_F32) static_cast<float*>(a.y)[o] = v;
-        else if (a.y_dtype == BAKRON_F16) from_f32(v, static_cast<__half*>(a.y)[o]);
-        else from_f32(v, static_cast<__nv_bfloat16*>(a.y)[o]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (i + r >= a.m) break;
+            if (a.y_dtype == BAKRON_F32) static_cast<float*>(a.y)[o + r] = v[r];
+            else if (a.y_dtype == BAKRON_F16) from_f32(v[r], static_cast<__half*>(a.y)[o + r]);
+            else from_f32(v[r], static_cast<__nv_bfloat16*>(a.y)[o + r]);
+        }
     }
     if (ck > 1) cluster.sync();
 }
