@@ -334,6 +334,13 @@ def _current_stream(index: int) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
+def _empty(rows, cols: int, dtype, device) -> torch.Tensor:
+    """A new rows x cols tensor, or cols without rows (the shortest way torch has to one)."""
+    if rows is None:
+        return torch.empty_strided((cols,), (1,), dtype=dtype, device=device)
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
 def _call(fn, device: int, stream, *args) -> int:
     """fn(*args, stream) with ``device`` current: the library launches on the current device."""
     if device == torch.cuda.current_device():
@@ -678,7 +685,7 @@ def pack4(codes, scales, group_size=None, unsigned: bool = False, stream=None,
     nbytes = bakron_pack4_bytes(m, n, g)
     if nbytes == 0:
         raise BakronError(BAKRON_ERR_INVALID_ARG, "bakron_pack4")
-    packed = codes.new_empty(nbytes, dtype=torch.uint8)
+    packed = _empty(None, nbytes, torch.uint8, codes.device)
     st, read = _status_of(status, codes.device, check)
     _raise(bakron_pack4(codes, scales, g, unsigned, packed, st, stream), "bakron_pack4")
     if read:
@@ -689,8 +696,9 @@ def pack4(codes, scales, group_size=None, unsigned: bool = False, stream=None,
 def unpack4(packed, m: int, n: int, group_size=None, unsigned: bool = False, stream=None):
     """(codes, scales) of a layer in the 4-bit layout; scales m, or m x G with a group size."""
     _, G = _steps(n, group_size)
-    codes = packed.new_empty((m, n), dtype=torch.int8)
-    scales = packed.new_empty((m,) if group_size is None else (m, G), dtype=torch.float32)
+    codes = _empty(m, n, torch.int8, packed.device)
+    scales = _empty(None, m, torch.float32, packed.device) if group_size is None else \
+        _empty(m, G, torch.float32, packed.device)
     _raise(bakron_unpack4(packed, group_size, unsigned, codes, scales, stream), "bakron_unpack4")
     return codes, scales
 
@@ -704,7 +712,7 @@ def matvec4(packed, m: int, n: int, x, group_size=None, codebook=None, x_scales=
         raise ValueError(f"x: expected {n} columns, got {tuple(shape)}")
     if out_dtype is None:
         out_dtype = torch.float32 if x.dtype == torch.int8 else x.dtype
-    y = x.new_empty((shape[0], m) if len(shape) == 2 else (m,), dtype=out_dtype)
+    y = _empty(shape[0] if len(shape) == 2 else None, m, out_dtype, x.device)
     code = _matvec4(packed, m, group_size, codebook, x, x_scales, x_group_size, y, m,
                     x.get_device(), stream)
     if code:
@@ -719,16 +727,18 @@ def rms_norm_q8(x, weight=None, eps: float = 1e-6, residual=None, group_size=Non
     group size. Rows that are not finite give NaN scales and, where the caller gives a ``status``
     word, BAKRON_ERR_NONFINITE in it."""
     shape = x.shape
-    _, G = _steps(shape[-1], group_size)
-    q = x.new_empty(shape, dtype=torch.int8)
-    scales = x.new_empty((shape[0], G) if len(shape) == 2 else (G,), dtype=torch.float32)
+    n = shape[-1]
+    _, G = _steps(n, group_size)
+    rows, device = shape[0] if len(shape) == 2 else None, x.device
+    q = _empty(rows, n, torch.int8, device)
+    scales = _empty(rows, G, torch.float32, device)
     if sum_out is not None:
         code = bakron_rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out, status,
                                   stream)
     else:
         if residual is not None:
-            sum_out = x.new_empty(shape)
-        code = _rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out, shape[-1],
+            sum_out = _empty(rows, n, x.dtype, device)
+        code = _rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out, n,
                             status, x.get_device(), stream)
     if code:
         raise BakronError(code, "bakron_rms_norm_q8")
@@ -743,15 +753,17 @@ def distill(logits, top_idx, top_logits, temperature: float = 1.0, teacher_lse=N
     unless ``grad``; ``dlogits`` names its buffer, which may be ``logits``). With the caller's own
     ``status`` word the call does not wait for the device."""
     shape = logits.shape
-    rows = 1 if len(shape) == 1 else shape[0]
-    loss = logits.new_empty(rows, dtype=torch.float32)
-    lse = logits.new_empty(rows, dtype=torch.float32)
-    st, read = (status, False) if status is not None else _status_of(None, logits.device, check)
+    rows, device = 1 if len(shape) == 1 else shape[0], logits.device
+    loss = _empty(None, rows, torch.float32, device)
+    lse = _empty(None, rows, torch.float32, device)
+    st, read = _status_of(status, device, check)
     if grad and dlogits is not None:
         code = bakron_distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature,
                               loss, lse, dlogits, st, stream)
     else:
-        dlogits = logits.new_empty(shape) if grad else None
+        dlogits = None
+        if grad:
+            dlogits = _empty(None if len(shape) == 1 else rows, shape[-1], logits.dtype, device)
         code = _distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature, loss,
                         lse, dlogits, shape[-1], st, logits.get_device(), stream)
     if code:
