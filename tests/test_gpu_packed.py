@@ -427,3 +427,13 @@ def test_streams_capture_and_replay(bk):
 def test_product_of_the_longest_rows(bk, x, book):
     """Activations that fill shared memory: fewer tokens a block."""
     _check_product(bk, 20, 65536, 9, x, "f32", 32, book, x_group=32 if x == "i8" else None, seed=2)
+
+
+@pytest.mark.parametrize("args", [["--op", "pack4"], ["--op", "matvec4", "--k", "3"],
+                                  ["--op", "matvec4", "--k", "1", "--dtype", "i8"],
+                                  ["--op", "rms_norm_q8", "--k", "5", "--group-size", "32"],
+                                  ["--op", "distill", "--k", "4", "--d", "1000", "--dtype", "f16"]])
+def test_kernel_bench_runs_the_serving_calls(bk, args, capsys):
+    from two_sided_adaptive_bakron_b200 import kernel_bench
+    assert kernel_bench.main(args + ["--workload", "small_64x128", "--iters", "2"]) == 0
+    assert " ms (mean of 1)" in capsys.readouterr().out
