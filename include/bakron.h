@@ -333,8 +333,8 @@ int bakron_unpack4(const void* packed, int m, int n, int group_size, int unsigne
  * (fp32 activations: 24 bits; with a codebook: entries to 22 bits for fp16 and 8-bit
  * activations, 16 for bf16, 24 for fp32), sums are fp32 (8-bit activations on the integer grid:
  * exact within 64 columns), and the result is rounded once to y's type.
- * Any number of tokens is right; the weights are read once for every 32 tokens (8 tokens of fp32),
- * so it is meant for few.
+ * Any number of tokens is right; the weights are read once for up to 32 tokens (8 tokens of fp32;
+ * fewer in layers of very long rows), so it is meant for few.
  *
  *   packed, m, n, group_size [in] as for bakron_pack4.
  *   codebook [in]  HOST pointer to 2^bits finite entries, copied during the call (the codes are
@@ -407,7 +407,7 @@ int bakron_rms_norm_q8(const void* x, int64_t ldx, const void* residual, int64_t
  *   loss, lse [out] rows fp32 each. A row without a present entry has loss 0 and gradient 0.
  *   dlogits  [out] rows x vocab of dtype, row stride ldd; NULL: no gradient. May be the buffer
  *                  of logits (with ldd = ld).
- *   rows, vocab [in] rows >= 0 (0 does nothing), vocab >= 1.
+ *   rows, vocab [in] 0 <= rows <= 2^30 (0 does nothing), vocab >= 1.
  *   dev_status [out] BAKRON_ERR_INVALID_ARG if an index is >= vocab (that entry counts as
  *                  absent).
  * Logits of -inf are entries of probability 0; a NaN, a +inf, or a row of nothing but -inf gives

@@ -372,3 +372,21 @@ def test_rows_of_nothing_but_the_lowest_value(bk, dt, rows):
         assert ((dz[1:, 4:].float() - 1 / V / tau).abs() <= 2 * HALF[dt] / V / tau + 1e-9).all()
         assert ((dz[1:, :4].float() - (1 / V - 0.25) / tau).abs() <= 2 * HALF[dt] / tau).all()
         assert torch.isfinite(loss[0]) and torch.isfinite(dz[0]).all()
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_drawn_cases(bk, seed):
+    rng = np.random.default_rng(3000 + seed)
+    rows = int(np.exp(rng.uniform(0, np.log(700))))
+    V = int(np.exp(rng.uniform(0, np.log(60000))))
+    k = min(1024, int(np.exp(rng.uniform(0, np.log(200)))))
+    rows = max(1, min(rows, 4_000_000 // V))
+    dt = ["f32", "f16", "bf16"][seed % 3]
+    z, idx, top, teacher = _problem(rows, V, min(k, V), dt, seed, repeat=k > V or seed % 5 == 0)
+    tau = [0.7, 1.0, 4.0][seed % 3]
+    mass = torch.logsumexp(teacher.double() / tau, dim=1).float() if seed % 2 else None
+    w = None
+    if seed % 4 == 1:
+        w = torch.from_numpy(rng.standard_normal(rows).astype(np.float32)).cuda()
+        w[rows // 2] = 0
+    _check(bk, z, idx.to(torch.int32) if seed % 3 else idx, top, tau, mass, w, dt=dt)

@@ -437,3 +437,67 @@ def test_kernel_bench_runs_the_serving_calls(bk, args, capsys):
     from two_sided_adaptive_bakron_b200 import kernel_bench
     assert kernel_bench.main(args + ["--workload", "small_64x128", "--iters", "2"]) == 0
     assert " ms (mean of 1)" in capsys.readouterr().out
+
+
+def _draw(rng, options):
+    return options[rng.integers(len(options))]
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_product_of_drawn_cases(bk, seed):
+    """Sizes, types, groups and tokens at random: slices that end anywhere, clusters, tails."""
+    rng = np.random.default_rng(1000 + seed)
+    m, n = int(np.exp(rng.uniform(0, np.log(3000)))), int(np.exp(rng.uniform(0, np.log(6000))))
+    tokens = int(np.exp(rng.uniform(0, np.log(40))))
+    x = _draw(rng, ["f32", "f16", "bf16", "i8"])
+    group = _draw(rng, [None, 32, 64, 96, 128, 160, 256, 320, 512, 1024])
+    book = _draw(rng, [None, None, BOOK16, BOOK16[:8], [-1.0, -0.25, 0.25, 1.0]])
+    xg = _draw(rng, [None, 32, 64, 96, 512]) if x == "i8" else None
+    _check_product(bk, m, n, tokens, x, _draw(rng, ["f32", "f16", "bf16"]) if x == "i8" else x,
+                   group if group is None or group < n else None, book,
+                   xg if xg is None or xg < n else None, seed=seed)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_norm_of_drawn_cases(bk, seed):
+    rng = np.random.default_rng(2000 + seed)
+    rows = int(np.exp(rng.uniform(0, np.log(900))))
+    n = int(np.exp(rng.uniform(0, np.log(20000))))
+    rows = max(1, min(rows, 2_000_000 // n))
+    if seed % 4 == 0:
+        rows, n = 700, 8 * int(rng.integers(1, 200))      # many rows of whole chunks
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    dt = DT[_draw(rng, ["f32", "f16", "bf16"])]
+    x = (torch.randn(rows, n, generator=gen, device="cuda") * _draw(rng, [1e-3, 1.0, 30.0])).to(dt)
+    x[rows // 2] = 0
+    r = _draw(rng, [None, torch.randn(rows, n, generator=gen, device="cuda").to(dt)])
+    w = _draw(rng, [None, torch.randn(n, generator=gen, device="cuda").to(dt),
+                    torch.randn(n, generator=gen, device="cuda")])
+    _check_norm(bk, x, w, r, _draw(rng, [None, 32, 64, 96, 128, 256, 384]))
+
+
+def test_calls_on_a_stream_own_what_they_write(bk):
+    """Outputs made for a named stream come from that stream's memory: what the current stream still
+    works on is not overwritten."""
+    codes, scales = _layer(64, 256, 32, 5)
+    layer = bk.PackedLayer(_cuda(codes), _cuda(scales), 32)
+    x = torch.randn(8, 256, device="cuda")
+    ref = layer.matvec(x)
+    idx, top = torch.zeros(8, 1, dtype=torch.int32, device="cuda"), torch.zeros(8, 1, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()                             # the inputs are there for every stream
+    for handle in (side, side.cuda_stream):
+        busy = torch.randn(4096, 4096, device="cuda")
+        keep = torch.ones(8, 64, device="cuda")
+        for _ in range(4):
+            busy = busy @ busy * 1e-3                    # the current stream is behind
+        late = keep + busy[:8, :64] * 0
+        ptr = keep.data_ptr()
+        del keep                                         # its memory is free for this stream only
+        y = layer.matvec(x, stream=handle)
+        q, s, _ = bk.rms_norm_q8(x, stream=handle)
+        loss, _, dz = bk.distill(x, idx, top, stream=handle)
+        side.synchronize()
+        assert y.data_ptr() != ptr and torch.equal(y, ref)
+        torch.cuda.synchronize()
+        assert (late == 1).all() or not torch.isfinite(busy).all()

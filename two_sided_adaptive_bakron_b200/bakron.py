@@ -17,6 +17,7 @@ the shared library is missing the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional
@@ -668,6 +669,21 @@ def proxy_loss(dW, H_O, H_I, stream=None) -> torch.Tensor:
     return loss
 
 
+def _on_stream(f):
+    """Runs a call that is given a ``stream`` with that stream current: what it allocates then
+    belongs to the stream that writes it, and nothing the current stream still uses is reused."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else \
+                torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
 def _status_of(status, device, check: bool):
     """(status word, whether to read it): the caller's own word is left to the caller."""
     if status is not None:
@@ -675,8 +691,9 @@ def _status_of(status, device, check: bool):
     return new_status(device), check
 
 
-def pack4(codes, scales, group_size=None, unsigned: bool = False, stream=None,
-          check: bool = True, status=None) -> torch.Tensor:
+@_on_stream
+def pack4(codes, scales, group_size=None, unsigned: bool = False, check: bool = True,
+          status=None) -> torch.Tensor:
     """The 4-bit layout of a layer's codes (m x n int8) and grid steps (m, or m x G with a
     group size); ``unsigned`` for codebook indices. With the caller's own ``status`` word the
     call does not wait for the device."""
@@ -687,24 +704,27 @@ def pack4(codes, scales, group_size=None, unsigned: bool = False, stream=None,
         raise BakronError(BAKRON_ERR_INVALID_ARG, "bakron_pack4")
     packed = _empty(None, nbytes, torch.uint8, codes.device)
     st, read = _status_of(status, codes.device, check)
-    _raise(bakron_pack4(codes, scales, g, unsigned, packed, st, stream), "bakron_pack4")
+    _raise(bakron_pack4(codes, scales, g, unsigned, packed, st), "bakron_pack4")
     if read:
-        _raise(bakron_read_status(st, stream), "bakron_pack4 (device)")
+        _raise(bakron_read_status(st, torch.cuda.current_stream(codes.device)),
+               "bakron_pack4 (device)")
     return packed
 
 
-def unpack4(packed, m: int, n: int, group_size=None, unsigned: bool = False, stream=None):
+@_on_stream
+def unpack4(packed, m: int, n: int, group_size=None, unsigned: bool = False):
     """(codes, scales) of a layer in the 4-bit layout; scales m, or m x G with a group size."""
     _, G = _steps(n, group_size)
     codes = _empty(m, n, torch.int8, packed.device)
     scales = _empty(None, m, torch.float32, packed.device) if group_size is None else \
         _empty(m, G, torch.float32, packed.device)
-    _raise(bakron_unpack4(packed, group_size, unsigned, codes, scales, stream), "bakron_unpack4")
+    _raise(bakron_unpack4(packed, group_size, unsigned, codes, scales), "bakron_unpack4")
     return codes, scales
 
 
+@_on_stream
 def matvec4(packed, m: int, n: int, x, group_size=None, codebook=None, x_scales=None,
-            x_group_size=None, out_dtype=None, stream=None) -> torch.Tensor:
+            x_group_size=None, out_dtype=None) -> torch.Tensor:
     """y = x W^T for a layer (m x n) in the 4-bit layout and x of one token (n) or a few (tokens x
     n); y has x's type (float32 for int8 x) unless ``out_dtype`` names another."""
     shape = x.shape
@@ -714,14 +734,15 @@ def matvec4(packed, m: int, n: int, x, group_size=None, codebook=None, x_scales=
         out_dtype = torch.float32 if x.dtype == torch.int8 else x.dtype
     y = _empty(shape[0] if len(shape) == 2 else None, m, out_dtype, x.device)
     code = _matvec4(packed, m, group_size, codebook, x, x_scales, x_group_size, y, m,
-                    x.get_device(), stream)
+                    x.get_device(), None)
     if code:
         raise BakronError(code, "bakron_matvec4")
     return y
 
 
+@_on_stream
 def rms_norm_q8(x, weight=None, eps: float = 1e-6, residual=None, group_size=None, sum_out=None,
-                status=None, stream=None):
+                status=None):
     """(q int8, scales, sum): the norm of x + residual in 8 bits, and the sum in x's type (None
     without a residual, unless ``sum_out`` asks for it). Scales: one per row, or rows x G with a
     group size. Rows that are not finite give NaN scales and, where the caller gives a ``status``
@@ -733,21 +754,20 @@ def rms_norm_q8(x, weight=None, eps: float = 1e-6, residual=None, group_size=Non
     q = _empty(rows, n, torch.int8, device)
     scales = _empty(rows, G, torch.float32, device)
     if sum_out is not None:
-        code = bakron_rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out, status,
-                                  stream)
+        code = bakron_rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out, status)
     else:
         if residual is not None:
             sum_out = _empty(rows, n, x.dtype, device)
         code = _rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out, n,
-                            status, x.get_device(), stream)
+                            status, x.get_device(), None)
     if code:
         raise BakronError(code, "bakron_rms_norm_q8")
     return q, scales, sum_out
 
 
+@_on_stream
 def distill(logits, top_idx, top_logits, temperature: float = 1.0, teacher_lse=None,
-            row_weights=None, grad: bool = True, dlogits=None, stream=None, check: bool = True,
-            status=None):
+            row_weights=None, grad: bool = True, dlogits=None, check: bool = True, status=None):
     """(loss, lse, dlogits) of the distillation from a teacher's top logits: per-row weighted KL,
     the student's log-sum-exp of logits / temperature, and the gradient of the summed loss (None
     unless ``grad``; ``dlogits`` names its buffer, which may be ``logits``). With the caller's own
@@ -759,17 +779,18 @@ def distill(logits, top_idx, top_logits, temperature: float = 1.0, teacher_lse=N
     st, read = _status_of(status, device, check)
     if grad and dlogits is not None:
         code = bakron_distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature,
-                              loss, lse, dlogits, st, stream)
+                              loss, lse, dlogits, st)
     else:
         dlogits = None
         if grad:
             dlogits = _empty(None if len(shape) == 1 else rows, shape[-1], logits.dtype, device)
         code = _distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature, loss,
-                        lse, dlogits, shape[-1], st, logits.get_device(), stream)
+                        lse, dlogits, shape[-1], st, logits.get_device(), None)
     if code:
         raise BakronError(code, "bakron_distill")
     if read:
-        _raise(bakron_read_status(st, stream), "bakron_distill (device)")
+        _raise(bakron_read_status(st, torch.cuda.current_stream(device)),
+               "bakron_distill (device)")
     return loss, lse, dlogits
 
 
@@ -786,16 +807,16 @@ class PackedLayer:
         self.m, self.n = codes.shape
         self.group_size = group_size
         self.codebook, _ = _codebook(codebook)
-        self.packed = pack4(codes, scales, group_size, codebook is not None, stream)
+        self.packed = pack4(codes, scales, group_size, codebook is not None, stream=stream)
 
     def matvec(self, x, x_scales=None, x_group_size=None, out_dtype=None, stream=None):
         return matvec4(self.packed, self.m, self.n, x, self.group_size, self.codebook, x_scales,
-                       x_group_size, out_dtype, stream)
+                       x_group_size, out_dtype, stream=stream)
 
     def unpack(self, stream=None):
         """(codes, scales) as they were given."""
         return unpack4(self.packed, self.m, self.n, self.group_size, self.codebook is not None,
-                       stream)
+                       stream=stream)
 
 
 class Solver:
@@ -917,8 +938,8 @@ class Solver:
 
     def packed(self, stream=None) -> PackedLayer:
         """The layer that the last ``run`` rounded, in 4 bits (for bits <= 4), with the grid steps,
-        group size and codebook of that run. After a run with ``incoherence`` it is the rotated
-        layer W~."""
+        group size and codebook of that run (the tensors that it was given, as they are now). After a
+        run with ``incoherence`` it is the rotated layer W~."""
         if self._steps is None:
             raise ValueError("no layer was rounded yet")
         return PackedLayer(self.codes, *self._steps, stream)

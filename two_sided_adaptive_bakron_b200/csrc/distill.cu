@@ -771,7 +771,8 @@ extern "C" int bakron_distill(const void* logits, int dtype, int rows, int vocab
                               float* lse, void* dlogits, int64_t ldd, int* dev_status,
                               void* stream) {
     if (!float_dtype(dtype) || !float_dtype(top_dtype) ||
-        (idx_dtype != BAKRON_I32 && idx_dtype != BAKRON_I64) || rows < 0 || vocab < 1 ||
+        (idx_dtype != BAKRON_I32 && idx_dtype != BAKRON_I64) || rows < 0 || rows > (1 << 30) ||
+        vocab < 1 ||
         ld < vocab || (dlogits && ldd < vocab) || (dlogits == logits && dlogits && ldd != ld) ||
         k < 1 || k > kMaxK || !(temperature > 0.f) || !std::isfinite(temperature) ||
         !std::isfinite(1.f / temperature))
