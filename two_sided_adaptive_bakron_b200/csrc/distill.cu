@@ -441,7 +441,7 @@ distill_rows_kernel(const X* z0, int rows, int V, int64_t ld, const Teacher T,
                     float* __restrict__ loss, float* __restrict__ lse, X* dz0, int64_t ldd,
                     int* __restrict__ status, int keep) {
     constexpr int N = Vec<X>::N, ALL = DATA + 32;
-    constexpr int kRegs = DATA == 992 ? 4 : 1;
+    constexpr int kRegs = DATA == 992 ? 4 : 0, kHeld = kRegs > 0 ? kRegs : 1;
     enum { kData = 1, kListReady = 2, kListFree = 4 };      // barriers (the last two: one a buffer)
     extern __shared__ __align__(16) char smem[];
     __shared__ float2 pairs[2][DATA / 32];
@@ -543,15 +543,22 @@ distill_rows_kernel(const X* z0, int rows, int V, int64_t ld, const Teacher T,
             if (extra >= 0) from_f32(0.f, dz[extra]);
             for (int i = tid; i < S.body; i += DATA) put(i, zero);
         };
-        // vectors of this thread behind those that are kept: a few at a time
-        const int first = (keep + kRegs) * DATA + tid;
+        // vectors of this thread behind those that are kept, four at a time: f(vector, the four, whether
+        // all of them are there)
         const auto stream = [&](auto f) {
-            for (int i = first; i < S.body; i += 4 * DATA) {
+            for (int base = (keep + kRegs) * DATA; base < S.body; base += 4 * DATA) {
+                const uint4* from = zv + base + tid;
                 uint4 v[4];
+                if (base + 4 * DATA <= S.body) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    v[u] = i + u * DATA < S.body ? zv[i + u * DATA] : Vec<X>::fill_low();
-                f(i, v);
+                    for (int u = 0; u < 4; ++u) v[u] = from[u * DATA];
+                    f(base + tid, v, true);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        v[u] = base + u * DATA + tid < S.body ? from[u * DATA] : Vec<X>::fill_low();
+                    f(base + tid, v, false);
+                }
             }
         };
 
@@ -583,8 +590,8 @@ distill_rows_kernel(const X* z0, int rows, int V, int64_t ld, const Teacher T,
                 }
                 s += part[0] + part[1];
             };
-            uint4 held[kRegs];
-            const bool hold = keep * DATA < S.body;
+            uint4 held[kHeld];
+            const bool hold = kRegs > 0 && keep * DATA < S.body;
             if (hold) {
 #pragma unroll
                 for (int u = 0; u < kRegs; ++u) {
@@ -592,7 +599,7 @@ distill_rows_kernel(const X* z0, int rows, int V, int64_t ld, const Teacher T,
                     held[u] = i < S.body ? zv[i] : Vec<X>::fill_low();
                 }
             }
-            stream([&](int, const uint4 (&v)[4]) { add(v); });
+            stream([&](int, const uint4 (&v)[4], bool) { add(v); });
             for (int q = 0; q < groups; ++q) {
                 wait(GRAD ? groups - 1 - q : groups - 1);
                 uint4 v[4];
@@ -636,18 +643,24 @@ distill_rows_kernel(const X* z0, int rows, int V, int64_t ld, const Teacher T,
                     put(i, x);
                 };
                 const bool plain = wide && ref.usual() && mass != 0.f;
+                // four whole rounds of plain vectors
+                const auto write4 = [&](int i, const uint4 (&v)[4]) {
+                    uint4* to = dv + i;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        float x[N];
+                        Vec<X>::get(v[u], x);
+#pragma unroll
+                        for (int k = 0; k < N; ++k) x[k] = fq * ex2(fmaf(x[k], c, -ref.R));
+                        __stcs(to + u * DATA, Vec<X>::put(x));
+                    }
+                };
                 for (int q = 0; q < groups; ++q) {
                     if (plain && 4 * q + 4 <= keep && (4 * q + 4) * DATA <= S.body) {
-                        const uint4* from = slot + 4 * q * DATA;
-                        uint4* to = dv + 4 * q * DATA + tid;
+                        uint4 v[4];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            float x[N];
-                            Vec<X>::get(from[u * DATA], x);
-#pragma unroll
-                            for (int k = 0; k < N; ++k) x[k] = fq * ex2(fmaf(x[k], c, -ref.R));
-                            __stcs(to + u * DATA, Vec<X>::put(x));
-                        }
+                        for (int u = 0; u < 4; ++u) v[u] = slot[(4 * q + u) * DATA];
+                        write4(4 * q * DATA + tid, v);
                     } else if (mass != 0.f) {
                         for (int u = 4 * q; u < min(4 * q + 4, keep); ++u)
                             if (u * DATA + tid < S.body) write(u * DATA + tid, slot[u * DATA]);
@@ -662,10 +675,14 @@ distill_rows_kernel(const X* z0, int rows, int V, int64_t ld, const Teacher T,
                             if (i < S.body) write(i, held[u]);
                         }
                     }
-                    stream([&](int i, const uint4 (&v)[4]) {
+                    stream([&](int i, const uint4 (&v)[4], bool all) {
+                        if (all && plain) {
+                            write4(i, v);
+                        } else {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            if (i + u * DATA < S.body) write(i + u * DATA, v[u]);
+                            for (int u = 0; u < 4; ++u)
+                                if (i + u * DATA < S.body) write(i + u * DATA, v[u]);
+                        }
                     });
                     if (extra >= 0) from_f32(fq * ref.term(zx), dz[extra]);
                     bar_sync(kData, DATA);
@@ -712,6 +729,8 @@ int launch_rows(const X* z, int rows, int V, int64_t ld, const Teacher& T, float
     const size_t vec = (size_t)DATA * 16;
     size_t keep = room > lists ? (room - lists) / vec : 0;
     keep = std::min({keep, (size_t)16, ((size_t)V / Vec<X>::N + DATA - 1) / DATA});
+    // whole groups of four, unless the row ends within them
+    if (keep * DATA < (size_t)V / Vec<X>::N) keep -= keep % 4;
     const size_t smem = keep * vec + lists;
     auto kern = dz ? distill_rows_kernel<X, DATA, true> : distill_rows_kernel<X, DATA, false>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
