@@ -543,21 +543,21 @@ distill_rows_kernel(const X* z0, int rows, int V, int64_t ld, const Teacher T,
             if (extra >= 0) from_f32(0.f, dz[extra]);
             for (int i = tid; i < S.body; i += DATA) put(i, zero);
         };
-        // vectors of this thread behind those that are kept, four at a time: f(vector, the four, whether
-        // all of them are there)
+        // vectors of this thread behind those that are kept: f(index, four of them) as long as every
+        // thread has four, then f(index, one)
         const auto stream = [&](auto f) {
             for (int base = (keep + kRegs) * DATA; base < S.body; base += 4 * DATA) {
                 const uint4* from = zv + base + tid;
-                uint4 v[4];
                 if (base + 4 * DATA <= S.body) {
+                    uint4 v[4];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) v[u] = from[u * DATA];
-                    f(base + tid, v, true);
+                    f(base + tid, v);
                 } else {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        v[u] = base + u * DATA + tid < S.body ? from[u * DATA] : Vec<X>::fill_low();
-                    f(base + tid, v, false);
+                    for (int i = base + tid; i < S.body; i += DATA) {
+                        const uint4 v[1] = {zv[i]};
+                        f(i, v);
+                    }
                 }
             }
         };
@@ -599,22 +599,32 @@ distill_rows_kernel(const X* z0, int rows, int V, int64_t ld, const Teacher T,
                     held[u] = i < S.body ? zv[i] : Vec<X>::fill_low();
                 }
             }
-            stream([&](int, const uint4 (&v)[4], bool) { add(v); });
+            stream([&](int, const auto& v) { add(v); });
             for (int q = 0; q < groups; ++q) {
                 wait(GRAD ? groups - 1 - q : groups - 1);
-                uint4 v[4];
-                if (4 * q + 4 <= keep && (4 * q + 4) * DATA <= S.body) {
+                // a whole group, one with most of its vectors (the others count as -inf), or the
+                // one or two that are left
+                const int have = min(4 * q + 4, keep);
+                if (have * DATA <= S.body && have == 4 * q + 4) {
+                    uint4 v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[k] = slot[(4 * q + k) * DATA];
-                } else {
+                    add(v);
+                } else if (min(have * DATA, S.body) > (4 * q + 2) * DATA) {
+                    uint4 v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int u = 4 * q + k;
                         v[k] = u < keep && u * DATA + tid < S.body ? slot[u * DATA]
                                                                    : Vec<X>::fill_low();
                     }
+                    add(v);
+                } else {
+                    for (int u = 4 * q; u < have && u * DATA + tid < S.body; ++u) {
+                        const uint4 v[1] = {slot[u * DATA]};
+                        add(v);
+                    }
                 }
-                add(v);
                 if (!GRAD) copy_group(next, q);
             }
             if (hold) add(held);
@@ -675,14 +685,16 @@ distill_rows_kernel(const X* z0, int rows, int V, int64_t ld, const Teacher T,
                             if (i < S.body) write(i, held[u]);
                         }
                     }
-                    stream([&](int i, const uint4 (&v)[4], bool all) {
-                        if (all && plain) {
-                            write4(i, v);
-                        } else {
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                if (i + u * DATA < S.body) write(i + u * DATA, v[u]);
+                    stream([&](int i, const auto& v) {
+                        constexpr int count = sizeof(v) / sizeof(uint4);
+                        if constexpr (count == 4) {
+                            if (plain) {
+                                write4(i, v);
+                                return;
+                            }
                         }
+#pragma unroll
+                        for (int u = 0; u < count; ++u) write(i + u * DATA, v[u]);
                     });
                     if (extra >= 0) from_f32(fq * ref.term(zx), dz[extra]);
                     bar_sync(kData, DATA);
