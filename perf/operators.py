@@ -283,7 +283,7 @@ def _own_run(st):
         loss, lse, grad = bk.distill(st["logits"], st["idx"], st["top"], c["tau"], teacher_lse=st["lse"],
                                      row_weights=st["weights"], grad=c["grad"], status=st["status"])
         return {"loss": loss, "lse": lse, "grad": grad} if c["grad"] else {"loss": loss, "lse": lse}
-    g = c["group"] or None
+    g = c["group"] or c["n"]        # steps stand as rows x steps, one step a row too
     packed = bk.pack4(st["codes"], st["steps"], group_size=g, unsigned=c["book"], status=st["status"])
     codes, steps = bk.unpack4(packed, c["m"], c["n"], group_size=g, unsigned=c["book"])
     return {"packed": packed, "codes": codes, "steps": steps}
