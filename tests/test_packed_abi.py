@@ -35,6 +35,12 @@ def test_layout_bytes(bk):
         assert bk.bakron_pack4_bytes(m, n, g) == 0
 
 
+def test_layout_bytes_of_the_binding(bk):
+    for m, n, g in [(1, 1, 1), (16, 64, 32), (17, 65, 32), (28672, 8192, 128), (5, 700, 96),
+                    (100, 65536, 32), (3, 50, 64)]:
+        assert bk._packed_bytes(m, n, bk._steps(n, g)[1]) == bk.bakron_pack4_bytes(m, n, g)
+
+
 def test_pack_refusals(L):
     def pack(codes=P, ldc=64, scales=P, m=8, n=64, g=32, u=0, packed=P, st=P):
         return L.bakron_pack4(codes, ldc, scales, m, n, g, u, packed, st, None)

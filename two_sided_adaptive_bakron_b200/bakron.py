@@ -360,6 +360,12 @@ def _steps(n: int, group_size) -> tuple[int, int]:
     return g, (1 if g >= n else -(-n // g))
 
 
+def _packed_bytes(m: int, n: int, G: int) -> int:
+    """bakron_pack4_bytes for G steps a row, without a call (and without its refusals)."""
+    mt = (m + 15) // 16
+    return mt * ((n + 63) // 64) * 512 + mt * G * 64
+
+
 def _codebook(codebook):
     """(ctypes array or None, bits) of a host codebook of 2, 4, 8 or 16 entries."""
     if codebook is None:
@@ -383,11 +389,10 @@ def bakron_pack4(codes, scales, group_size, unsigned_codes, packed, dev_status,
     if codes.dtype != torch.int8:
         raise ValueError(f"codes: expected torch.int8, got {codes.dtype}")
     g, G = _steps(n, group_size)
-    L = lib()
-    return _call(L.bakron_pack4, dev, stream, codes.data_ptr(), ldc,
+    return _call(lib().bakron_pack4, dev, stream, codes.data_ptr(), ldc,
                  _flat(scales, torch.float32, m * G, "scales", dev), m, n, g,
                  int(bool(unsigned_codes)),
-                 _flat(packed, torch.uint8, L.bakron_pack4_bytes(m, n, g), "packed", dev),
+                 _flat(packed, torch.uint8, _packed_bytes(m, n, G), "packed", dev),
                  _flat(dev_status, torch.int32, 1, "dev_status", dev))
 
 
@@ -397,9 +402,8 @@ def bakron_unpack4(packed, group_size, unsigned_codes, codes, scales, stream=Non
     if codes.dtype != torch.int8:
         raise ValueError(f"codes: expected torch.int8, got {codes.dtype}")
     g, G = _steps(n, group_size)
-    L = lib()
-    return _call(L.bakron_unpack4, dev, stream,
-                 _flat(packed, torch.uint8, L.bakron_pack4_bytes(m, n, g), "packed", dev), m, n, g,
+    return _call(lib().bakron_unpack4, dev, stream,
+                 _flat(packed, torch.uint8, _packed_bytes(m, n, G), "packed", dev), m, n, g,
                  int(bool(unsigned_codes)), codes.data_ptr(), ldc,
                  _flat(scales, torch.float32, m * G, "scales", dev))
 
@@ -418,18 +422,14 @@ def bakron_matvec4(packed, group_size, codebook, x, x_scales, x_group_size, y,
 def _matvec4(packed, m, group_size, codebook, x, x_scales, x_group_size, y, ldy, dev, stream):
     """bakron_matvec4 for a y that is known to have the rows of x, m columns and stride ldy."""
     tokens, n, ldx = _rows(x, "x", dev)
-    g, _ = _steps(n, group_size)
-    L = lib()
-    nbytes = L.bakron_pack4_bytes(m, n, g)
-    if nbytes == 0:
-        return BAKRON_ERR_INVALID_ARG
+    g, G = _steps(n, group_size)
     cb, bits = (None, 0) if codebook is None else _codebook(codebook)
     gx, xs = n, None
     if x_scales is not None:
         gx, Gx = _steps(n, x_group_size)
         xs = _flat(x_scales, torch.float32, tokens * Gx, "x_scales", dev)
-    return _call(L.bakron_matvec4, dev, stream, _flat(packed, torch.uint8, nbytes, "packed", dev),
-                 m, n, g, cb, bits, x.data_ptr(), _dtype(x, "x"), ldx, xs, gx, tokens,
+    return _call(lib().bakron_matvec4, dev, stream,
+                 _flat(packed, torch.uint8, _packed_bytes(m, n, G), "packed", dev), m, n, g, cb, bits, x.data_ptr(), _dtype(x, "x"), ldx, xs, gx, tokens,
                  y.data_ptr(), _dtype(y, "y"), ldy)
 
 
@@ -698,15 +698,13 @@ def pack4(codes, scales, group_size=None, unsigned: bool = False, check: bool = 
     group size); ``unsigned`` for codebook indices. With the caller's own ``status`` word the
     call does not wait for the device."""
     m, n = codes.shape
-    g, _ = _steps(n, group_size)
-    nbytes = bakron_pack4_bytes(m, n, g)
-    if nbytes == 0:
-        raise BakronError(BAKRON_ERR_INVALID_ARG, "bakron_pack4")
-    packed = _empty(None, nbytes, torch.uint8, codes.device)
-    st, read = _status_of(status, codes.device, check)
-    _raise(bakron_pack4(codes, scales, g, unsigned, packed, st), "bakron_pack4")
+    _, G = _steps(n, group_size)
+    device = codes.device
+    packed = _empty(None, _packed_bytes(m, n, G), torch.uint8, device)
+    st, read = _status_of(status, device, check)
+    _raise(bakron_pack4(codes, scales, group_size, unsigned, packed, st), "bakron_pack4")
     if read:
-        _raise(bakron_read_status(st, torch.cuda.current_stream(codes.device)),
+        _raise(bakron_read_status(st, torch.cuda.current_stream(device)),
                "bakron_pack4 (device)")
     return packed
 
@@ -715,9 +713,10 @@ def pack4(codes, scales, group_size=None, unsigned: bool = False, check: bool = 
 def unpack4(packed, m: int, n: int, group_size=None, unsigned: bool = False):
     """(codes, scales) of a layer in the 4-bit layout; scales m, or m x G with a group size."""
     _, G = _steps(n, group_size)
-    codes = _empty(m, n, torch.int8, packed.device)
-    scales = _empty(None, m, torch.float32, packed.device) if group_size is None else \
-        _empty(m, G, torch.float32, packed.device)
+    device = packed.device
+    codes = _empty(m, n, torch.int8, device)
+    scales = _empty(None if group_size is None else m, m if group_size is None else G, torch.float32,
+                    device)
     _raise(bakron_unpack4(packed, group_size, unsigned, codes, scales), "bakron_unpack4")
     return codes, scales
 
