@@ -21,6 +21,10 @@
 // c z - R in one rounding (fma): what R's rounding and c's are off cancels between a logit and the
 // sum it is divided by, so nothing large is lost in log p - log q. ex2.approx is good to 2 units in
 // the last place.
+//
+// Measured: 2048 rows of 131072 bf16, 64 entries: 252 us with the gradient (4.2 TB/s), 116 without (4.6);
+// 1024 of 131072 fp32 239 and 98 (5.5); 2048 of 32000 bf16 70 and 44. No unit is near its limit there;
+// 1024 entries a row, which one warp reads, take 574 and 530.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -763,7 +767,7 @@ int plan(const void* z_, int rows, int V, int64_t ld, const Teacher& T, float* l
     const int sms = tc::sm_count();
     if (sms <= 0) return BAKRON_ERR_CUDA;
     // Many rows: eight blocks of 128 threads an SM up to 24 KB a row, then two of 512, and one of 992
-    // above 384 KB, where two rows an SM would read most of themselves twice (measured with the
+    // above 384 KB, where two rows an SM would read most of themselves twice (measured when chosen, with the
     // gradient, 512 / 992 threads: 260 / 280 us for 2048 rows of 256 KB, 293 / 239 us for 1024 of
     // 512 KB; four blocks of 256 for 64 KB took 76 us, two of 512 take 72).
     if (rows >= 2 * sms) {
