@@ -429,8 +429,9 @@ def _matvec4(packed, m, group_size, codebook, x, x_scales, x_group_size, y, ldy,
         gx, Gx = _steps(n, x_group_size)
         xs = _flat(x_scales, torch.float32, tokens * Gx, "x_scales", dev)
     return _call(lib().bakron_matvec4, dev, stream,
-                 _flat(packed, torch.uint8, _packed_bytes(m, n, G), "packed", dev), m, n, g, cb, bits, x.data_ptr(), _dtype(x, "x"), ldx, xs, gx, tokens,
-                 y.data_ptr(), _dtype(y, "y"), ldy)
+                 _flat(packed, torch.uint8, _packed_bytes(m, n, G), "packed", dev), m, n, g, cb,
+                 bits, x.data_ptr(), _dtype(x, "x"), ldx, xs, gx, tokens, y.data_ptr(),
+                 _dtype(y, "y"), ldy)
 
 
 def bakron_rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out=None,

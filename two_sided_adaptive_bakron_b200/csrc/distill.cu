@@ -767,9 +767,9 @@ int plan(const void* z_, int rows, int V, int64_t ld, const Teacher& T, float* l
     const int sms = tc::sm_count();
     if (sms <= 0) return BAKRON_ERR_CUDA;
     // Many rows: eight blocks of 128 threads an SM up to 24 KB a row, then two of 512, and one of 992
-    // above 384 KB, where two rows an SM would read most of themselves twice (measured when chosen, with the
-    // gradient, 512 / 992 threads: 260 / 280 us for 2048 rows of 256 KB, 293 / 239 us for 1024 of
-    // 512 KB; four blocks of 256 for 64 KB took 76 us, two of 512 take 72).
+    // above 384 KB, where two rows an SM would read most of themselves twice (measured when chosen,
+    // with the gradient, 512 / 992 threads: 260 / 280 us for 2048 rows of 256 KB, 293 / 239 us for
+    // 1024 of 512 KB; four blocks of 256 for 64 KB took 76 us, two of 512 take 72).
     if (rows >= 2 * sms) {
         const size_t row = (size_t)V * sizeof(X);
         if (row <= 24 * 1024)

@@ -637,9 +637,9 @@ int launch(const Args& a, int ck, size_t smem, cudaStream_t st) {
 }
 
 // One way to cut the work: ck slices of the columns, the row tiles dealt out over clusters of ck
-// blocks, as many as fit the GPU at once (times the chunks of tokens). 28672 x 8192 of bf16 in 1 / 2 / 4
-// / 8 slices: one token 28.9 / 29.3 / 31.7 / 33.8 us, 8 tokens 31.3 / 31.8 / 34.6 / 43.4, and 16 tokens,
-// whose activations do not fit in one slice, 53.3 / 54.4 / 45.1 / 56.3.
+// blocks, as many as fit the GPU at once (times the chunks of tokens). 28672 x 8192 of bf16 in 1, 2,
+// 4 and 8 slices: one token 28.9 / 29.3 / 31.7 / 33.8 us, 8 tokens 31.3 / 31.8 / 34.6 / 43.4, and 16
+// tokens, whose activations do not fit in one slice, 53.3 / 54.4 / 45.1 / 56.3.
 struct Cut { int ck = 0, slice, pitch, chunk, clusters, max_tiles; size_t smem; double cost; };
 
 template <int K>
