@@ -8,6 +8,7 @@
 #define BAKRON_INTERNAL_H_
 
 #include <stddef.h>
+#include <stdint.h>
 
 #ifdef __cplusplus
 extern "C" {
@@ -30,6 +31,13 @@ int bakron_internal_proxy_loss_simt(const float* dW, int m, int n, const float* 
 /* Writes the order-28 Hadamard matrix the transform of bakron_rht uses (row-major, 784 HOST
  * bytes of +1 / -1). Host only; no device work. */
 void bakron_internal_hadamard28(signed char* out);
+
+/* How bakron_matvec4 would cut a call on a GPU of `sms` SMs (valid arguments, not checked; `book`:
+ * with a codebook). Writes to out[8] (HOST): dynamic shared memory of a block in bytes, blocks of a
+ * cluster, column tiles of a block, tokens of a block, clusters, row tiles of a cluster, 8-column
+ * product tiles, warps of a block. Host only; no device work. */
+int bakron_internal_matvec4_plan(int m, int n, int group_size, int x_dtype, int x_group_size,
+                                 int y_dtype, int book, int tokens, int sms, int64_t* out);
 
 #ifdef __cplusplus
 }

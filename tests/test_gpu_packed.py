@@ -501,3 +501,36 @@ def test_calls_on_a_stream_own_what_they_write(bk):
         assert y.data_ptr() != ptr and torch.equal(y, ref)
         torch.cuda.synchronize()
         assert (late == 1).all() or not torch.isfinite(busy).all()
+
+
+# products whose blocks take all of shared memory, or all but a little
+@pytest.mark.parametrize("m,n,group,tokens,x,book", [
+    (28672, 8192, None, 16, "bf16", False), (28672, 8192, None, 9, "f16", True),
+    (14336, 4096, None, 17, "bf16", True), (512, 18432, 64, 32, "bf16", False),
+    (4096, 5184, 64, 20, "f32", False), (4096, 11008, 128, 5, "f32", True),
+    (8192, 8192, 128, 33, "bf16", False), (28672, 8192, 128, 32, "i8", False)])
+def test_product_in_full_blocks(bk, m, n, group, tokens, x, book):
+    """Against fp64 products of the unpacked layer on the device."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    codes = torch.randint(0 if book else -8, 16 if book else 8, (m, n), generator=gen, device="cuda",
+                          dtype=torch.int8)
+    g = group or n
+    scales = torch.rand((m, -(-n // g)), generator=gen, device="cuda") + 0.5
+    if x == "i8":
+        xt = torch.randint(-127, 128, (tokens, n), generator=gen, device="cuda", dtype=torch.int8)
+        xs = torch.rand((tokens, 1), generator=gen, device="cuda") + 0.5
+        xd = xt.double() * xs.double()
+    else:
+        xt, xs = torch.randn((tokens, n), generator=gen, device="cuda").to(DT[x]), None
+        xd = xt.double()
+    got = bk.PackedLayer(codes, scales, group, BOOK16 if book else None).matvec(
+        xt, x_scales=xs, out_dtype=torch.float32)
+    carry = 0.0 if not book else {"f32": 2.0 ** -23, "bf16": 2.0 ** -16}.get(x, 2.0 ** -22)
+    table = torch.tensor(BOOK16, device="cuda").double()
+    for lo in range(0, m, 4096):
+        c = codes[lo:lo + 4096]
+        W = (table[c.int()] if book else c.double()) * \
+            scales[lo:lo + 4096].double().repeat_interleave(g, dim=1)[:, :n]
+        ref, a = xd @ W.T, xd.abs() @ W.abs().T
+        tol = 2.0 ** -24 * ref.abs() + a * (carry + (n / 64 + 24) * 2.0 ** -23)
+        assert ((got[:, lo:lo + 4096].double() - ref).abs() <= tol).all()

@@ -87,6 +87,7 @@ _SIGNATURES = {
                                         _c_int, _vp, _c_size_t, _vp, _vp]),
     "bakron_internal_proxy_loss_simt_workspace_bytes": (_c_size_t, [_c_int, _c_int]),
     "bakron_internal_hadamard28": (None, [_vp]),
+    "bakron_internal_matvec4_plan": (_c_int, [_c_int] * 9 + [_vp]),
     "bakron_internal_proxy_loss_simt": (_c_int, [_vp, _c_int, _c_int, _vp, _vp, _vp, _vp,
                                                  _c_size_t, _vp]),
 }
@@ -505,6 +506,22 @@ def _distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature,
                  temperature, loss.data_ptr(), lse.data_ptr(),
                  None if dlogits is None else dlogits.data_ptr(), ldd,
                  _flat(dev_status, torch.int32, 1, "dev_status", dev))
+
+
+def internal_matvec4_plan(m, n, x_dtype, group_size=None, x_group_size=None, out_dtype=None,
+                          book=False, tokens=1, sms=148):
+    """How bakron_matvec4 cuts a call on a GPU of ``sms`` SMs (host only), as a dict; None where it
+    refuses one."""
+    out = (ctypes.c_int64 * 8)()
+    g, _ = _steps(n, group_size)
+    gx, _ = _steps(n, x_group_size)
+    if out_dtype is None:
+        out_dtype = torch.float32 if x_dtype == torch.int8 else x_dtype
+    if lib().bakron_internal_matvec4_plan(m, n, g, _DTYPES[x_dtype], gx, _DTYPES[out_dtype],
+                                          int(book), tokens, sms, out):
+        return None
+    return dict(zip(("smem", "cluster", "slice", "chunk", "clusters", "max_tiles", "product_tiles",
+                     "warps"), out))
 
 
 def internal_hadamard28():

@@ -38,6 +38,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "bakron_internal.h"
 #include "pack4.cuh"
 #include "tcgemm_host.cuh"
 
@@ -47,6 +48,9 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kStages = 2;
+// Shared memory of a block, static arrays included: the kernel has none, all of it is laid out in the
+// dynamic part.
+constexpr size_t kSmemLimit = 227 * 1024;
 
 enum Kind { kF16, kBf16, kF32, kI8, kF16Book, kBf16Book, kF32Book };
 constexpr bool is_book(int k) { return k >= kF16Book; }
@@ -265,7 +269,6 @@ matvec4_kernel(const __grid_constant__ Args a) {
     constexpr bool HALF = STEPS == kAnywhere;
     constexpr int kWarps = warps_of(K), kThreads = kWarps * 32;
     extern __shared__ __align__(128) char smem[];
-    __shared__ int head_tile[kWarps];      // the tile that a warp ends but did not begin
     cg::cluster_group cluster = cg::this_cluster();
     const int ck = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int lane = threadIdx.x & 31, g = lane / 4, t = lane % 4;
@@ -287,8 +290,10 @@ matvec4_kernel(const __grid_constant__ Args a) {
     if constexpr (is_book(K)) at += planes(K) * 32768;
     const int rows = a.max_tiles * 16;
     float* part = reinterpret_cast<float*>(at);           // [kTok][rows]
-    float* head = part + kTok * rows;                     // [warp][kTok][16]
-    float* sxs = head + kWarps * kTok * 16;               // [kTok][steps of x in the slice]
+    float* head = part + kTok * rows;                     // [warp - 1][kTok][16]
+    int* head_tile = reinterpret_cast<int*>(head + (kWarps - 1) * kTok * 16);   // the tile that a
+                                                          // warp ends but did not begin (or -1)
+    float* sxs = reinterpret_cast<float*>(head_tile + kWarps);   // [kTok][steps of x in the slice]
     const int xg0 = a.Gx > 1 ? kt0 * 64 / a.gx : 0;
 
     if constexpr (K == kF32 || K == kF32Book) {
@@ -543,8 +548,8 @@ matvec4_kernel(const __grid_constant__ Args a) {
         }
         if (++c_batch == batches || unit + 1 == u1) {
             // the tile's sums: whole tiles and a tile's first part to its rows, the end of a tile
-            // that another warp began to this warp's place
-            float* out = whole ? part + (c_tile - rt0) * 16 : head + warp * kTok * 16;
+            // that another warp began to this warp's place (the first warp begins all of its own)
+            float* out = whole ? part + (c_tile - rt0) * 16 : head + (warp - 1) * kTok * 16;
             const int ld = whole ? rows : 16;
 #pragma unroll
             for (int q = 0; q < NT; ++q) {
@@ -574,7 +579,7 @@ matvec4_kernel(const __grid_constant__ Args a) {
         const int tile = head_tile[w];
         if (tile < 0) continue;
         for (int e = threadIdx.x; e < kTok * 16; e += kThreads)
-            part[(e / 16) * rows + tile * 16 + e % 16] += head[w * kTok * 16 + e];
+            part[(e / 16) * rows + tile * 16 + e % 16] += head[(w - 1) * kTok * 16 + e];
     }
 
     // the blocks of the cluster add up a share of the rows each, four rows a thread
@@ -653,11 +658,11 @@ Cut cut(const Args& a, int ck, int nt, int sms) {
     const int row = c.slice * 64 * (K == kI8 ? 1 : 2);
     c.pitch = K == kI8 ? row + 32 : row % 128 ? row : row + 64;
     const int tok = nt * tile_tokens(K);
-    const size_t limit = 227 * 1024;
+    const size_t limit = kSmemLimit;
     const auto bytes = [&] {
         size_t b = (size_t)warps_of(K) * kStages * (kBatch * 512 + a.batch_groups * 64) +
                    (size_t)c.chunk * token_rows(K) * c.pitch +
-                   (size_t)tok * 16 * 4 * (c.max_tiles + warps_of(K));
+                   (size_t)tok * 16 * 4 * (c.max_tiles + warps_of(K) - 1) + warps_of(K) * 4;
         if (is_book(K)) b += planes(K) * 32768;
         if (a.Gx > 1) b += (size_t)tok * 4 * ((size_t)c.slice * 64 / a.gx + 2);
         return b;
@@ -690,10 +695,9 @@ Cut cut(const Args& a, int ck, int nt, int sms) {
     return c;
 }
 
+// The cheapest cut for a call on `sms` SMs, also entered in its arguments, and its product tiles nt.
 template <int K>
-int plan(Args& a, cudaStream_t st) {
-    const int sms = tc::sm_count();
-    if (sms <= 0) return BAKRON_ERR_CUDA;
+Cut choose(Args& a, int sms, int& best_nt) {
     const Pack4Shape P(a.m, a.n, a.G);
     constexpr int kBatch = batch_of(K), cols = kBatch * 64;
     a.batch_groups = a.G == 1 || a.gs % cols == 0 ? 1
@@ -701,7 +705,7 @@ int plan(Args& a, cudaStream_t st) {
                                                   : (cols - 1) / a.gs + 2;
     a.batch_gq = cols / a.gs, a.batch_gr = cols % a.gs;
     Cut best;
-    int best_nt = 1;
+    best_nt = 1;
     for (int nt = 1; nt <= 4; nt *= 2) {
         if (nt > 1 && a.tokens <= nt / 2 * tile_tokens(K)) break;
         for (int ck = 1; ck <= 8 && (ck == 1 || P.kt >= kBatch * ck); ck *= 2) {
@@ -709,10 +713,21 @@ int plan(Args& a, cudaStream_t st) {
             if (c.ck && (!best.ck || c.cost < best.cost)) best = c, best_nt = nt;
         }
     }
-    if (!best.ck) return BAKRON_ERR_INVALID_ARG;
+    if (!best.ck) return best;
     a.slice = best.slice, a.pitch = best.pitch, a.chunk = best.chunk;
     a.clusters = best.clusters, a.max_tiles = best.max_tiles;
     a.tiles_each = P.mt / a.clusters, a.tiles_rest = P.mt % a.clusters;
+    return best;
+}
+
+template <int K>
+int plan(Args& a, cudaStream_t st) {
+    const int sms = tc::sm_count();
+    if (sms <= 0) return BAKRON_ERR_CUDA;
+    constexpr int cols = batch_of(K) * 64;
+    int best_nt;
+    const Cut best = choose<K>(a, sms, best_nt);
+    if (!best.ck) return BAKRON_ERR_INVALID_ARG;
     const int ck = best.ck;
     const size_t smem = best.smem;
     // batches begin at multiples of `cols` columns
@@ -783,6 +798,38 @@ void split_book(const float* c, int entries, Args& a) {
     }
 }
 
+Args arguments(const void* packed, int m, int n, int group_size, const void* x, int x_dtype,
+               int64_t ldx, const float* x_scales, int x_group_size, int tokens, void* y,
+               int y_dtype, int64_t ldy) {
+    Args a{};
+    a.packed = static_cast<const uint8_t*>(packed);
+    a.m = m, a.n = n;
+    a.G = group_count(group_size, n);
+    a.gs = a.G > 1 ? group_size : 1 << 30;     // one step: no column is past it
+    a.x = x, a.x_dtype = x_dtype, a.ldx = ldx, a.xs = x_scales;
+    a.Gx = x_dtype == BAKRON_I8 ? group_count(x_group_size, n) : 1;
+    a.gx = a.Gx > 1 ? x_group_size : 64 * ((n + 63) / 64);
+    a.tokens = tokens, a.y = y, a.y_dtype = y_dtype, a.ldy = ldy;
+    a.out1 = a.out2 = 1.f;
+    return a;
+}
+
+// f(the kind that a call takes)
+template <class F>
+int with_kind(const Args& a, bool book, F f) {
+    if (book) {
+        if (a.x_dtype == BAKRON_F32) return f(std::integral_constant<int, kF32Book>());
+        if (a.x_dtype == BAKRON_BF16) return f(std::integral_constant<int, kBf16Book>());
+        return f(std::integral_constant<int, kF16Book>());
+    }
+    switch (a.x_dtype) {
+        case BAKRON_F32: return f(std::integral_constant<int, kF32>());
+        case BAKRON_F16: return f(std::integral_constant<int, kF16>());
+        case BAKRON_BF16: return f(std::integral_constant<int, kBf16>());
+        default: return f(std::integral_constant<int, kI8>());
+    }
+}
+
 }  // namespace
 }  // namespace bakron
 
@@ -804,35 +851,30 @@ extern "C" int bakron_matvec4(const void* packed, int m, int n, int group_size,
     if (!packed || !x || !y || i8 != (x_scales != nullptr) || !aligned_to(packed, 16) ||
         !aligned_to(x, dtype_bytes(x_dtype)) || !aligned_to(y, dtype_bytes(y_dtype)))
         return BAKRON_ERR_INVALID_ARG;
-    Args a{};
-    a.packed = static_cast<const uint8_t*>(packed);
-    a.m = m, a.n = n;
-    a.G = group_count(group_size, n);
-    a.gs = a.G > 1 ? group_size : 1 << 30;     // one step: no column is past it
-    a.x = x, a.x_dtype = x_dtype, a.ldx = ldx, a.xs = x_scales;
-    a.Gx = i8 ? group_count(x_group_size, n) : 1;
-    a.gx = a.Gx > 1 ? x_group_size : 64 * ((n + 63) / 64);
-    a.tokens = tokens, a.y = y, a.y_dtype = y_dtype, a.ldy = ldy;
-    a.out1 = a.out2 = 1.f;
+    Args a = arguments(packed, m, n, group_size, x, x_dtype, ldx, x_scales, x_group_size, tokens, y,
+                       y_dtype, ldy);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (codebook) {
-        if (x_dtype == BAKRON_F32) {
-            split_book<kF32Book>(codebook, 1 << bits, a);
-            return plan<kF32Book>(a, st);
-        }
-        if (x_dtype == BAKRON_BF16) {
-            split_book<kBf16Book>(codebook, 1 << bits, a);
-            return plan<kBf16Book>(a, st);
-        }
-        split_book<kF16Book>(codebook, 1 << bits, a);
-        return plan<kF16Book>(a, st);
-    }
-    switch (x_dtype) {
-        case BAKRON_F32: return plan<kF32>(a, st);
-        case BAKRON_F16: return plan<kF16>(a, st);
-        case BAKRON_BF16: return plan<kBf16>(a, st);
-        default:
-            a.out1 = 1.f / 16.f;      // the codes stand in the upper halves of their bytes
-            return plan<kI8>(a, st);
-    }
+    return with_kind(a, codebook != nullptr, [&](auto kind) {
+        constexpr int K = decltype(kind)::value;
+        if constexpr (is_book(K)) split_book<K>(codebook, 1 << bits, a);
+        if constexpr (K == kI8) a.out1 = 1.f / 16.f;    // the codes stand in the upper halves of bytes
+        return plan<K>(a, st);
+    });
+}
+
+extern "C" int bakron_internal_matvec4_plan(int m, int n, int group_size, int x_dtype,
+                                            int x_group_size, int y_dtype, int book, int tokens,
+                                            int sms, int64_t* out) {
+    Args a = arguments(nullptr, m, n, group_size, nullptr, x_dtype, n, nullptr, x_group_size, tokens,
+                       nullptr, y_dtype, m);
+    return with_kind(a, book != 0, [&](auto kind) {
+        constexpr int K = decltype(kind)::value;
+        int nt;
+        const Cut c = choose<K>(a, sms, nt);
+        if (!c.ck) return (int)BAKRON_ERR_INVALID_ARG;
+        const int64_t r[8] = {(int64_t)c.smem, c.ck, c.slice, c.chunk, c.clusters, c.max_tiles, nt,
+                              warps_of(K)};
+        std::copy(r, r + 8, out);
+        return (int)BAKRON_OK;
+    });
 }
