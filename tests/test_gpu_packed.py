@@ -534,3 +534,19 @@ def test_product_in_full_blocks(bk, m, n, group, tokens, x, book):
         ref, a = xd @ W.T, xd.abs() @ W.abs().T
         tol = 2.0 ** -24 * ref.abs() + a * (carry + (n / 64 + 24) * 2.0 ** -23)
         assert ((got[:, lo:lo + 4096].double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("m,n,tokens", [(128, 65536, 16), (880, 55360, 8), (2000, 65536, 1),
+                                        (4096, 60000, 3)])
+def test_product_of_the_longest_rows_of_many_tiles(bk, m, n, tokens):
+    """fp32 activations, a codebook and steps of 32 columns: the sums of few row tiles fit."""
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    codes = torch.randint(0, 16, (m, n), generator=gen, device="cuda", dtype=torch.int8)
+    scales = torch.rand((m, -(-n // 32)), generator=gen, device="cuda") + 0.5
+    xt = torch.randn((tokens, n), generator=gen, device="cuda")
+    got = bk.PackedLayer(codes, scales, 32, BOOK16).matvec(xt)
+    W = torch.tensor(BOOK16, device="cuda").double()[codes.int()]
+    W *= scales.double().repeat_interleave(32, dim=1)[:, :n]
+    ref, a = xt.double() @ W.T, xt.double().abs() @ W.abs().T
+    tol = 2.0 ** -24 * ref.abs() + a * (2.0 ** -23 + (n / 64 + 24) * 2.0 ** -23)
+    assert ((got.double() - ref).abs() <= tol).all()

@@ -62,3 +62,16 @@ def test_every_plan_launches(bk, x, book):
                         continue
                     _check(bk, m, n, x_dtype=x, group_size=group, book=book, tokens=tokens,
                            x_group_size=32 if x == torch.int8 and tokens % 2 else None)
+
+
+# the longest rows, whose activations leave room for the sums of few row tiles
+@pytest.mark.parametrize("x", TYPES)
+@pytest.mark.parametrize("book", [False, True])
+def test_the_longest_rows_are_not_refused(bk, x, book):
+    for m in (1, 20, 128, 880, 1456, 2000, 4096, 32000):
+        for n in (55360, 60000, 65535, 65536):
+            for group in (None, 32, 64):
+                for tokens in (1, 2, 8, 16, 33, 40):
+                    if m * n < 2 ** 31:
+                        _check(bk, m, n, x_dtype=x, group_size=group, book=book, tokens=tokens,
+                               x_group_size=32)

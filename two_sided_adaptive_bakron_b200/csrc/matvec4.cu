@@ -648,7 +648,7 @@ int launch(const Args& a, int ck, size_t smem, cudaStream_t st) {
 struct Cut { int ck = 0, slice, pitch, chunk, clusters, max_tiles; size_t smem; double cost; };
 
 template <int K>
-Cut cut(const Args& a, int ck, int nt, int sms) {
+Cut cut(const Args& a, int ck, int nt, int sms, bool few_tiles) {
     const Pack4Shape P(a.m, a.n, a.G);
     constexpr int kBatch = batch_of(K);
     Cut c;
@@ -667,13 +667,21 @@ Cut cut(const Args& a, int ck, int nt, int sms) {
         if (a.Gx > 1) b += (size_t)tok * 4 * ((size_t)c.slice * 64 / a.gx + 2);
         return b;
     };
+    // tiles an SM goes through, and its share of staged activations (from L2)
+    const auto taken = [&] {
+        const long long chunks = (a.tokens + c.chunk - 1) / c.chunk;
+        const long long per_sm = ((long long)c.clusters * ck * chunks + sms - 1) / sms;
+        c.ck = ck;
+        c.cost = (double)per_sm * (c.max_tiles * (double)c.slice +
+                                   0.08 * c.slice * c.chunk * token_rows(K) + 4.0);
+    };
     c.chunk = std::min(a.tokens, tok);
     // SMs that clusters of ck blocks can fill (they do not cross a GPC): 132 of 148 in fours, 120 in
     // eights, as the occupancy query says; one more would wait for a second wave
     const int fit = ck <= 2 ? sms : ck == 4 ? sms * 33 / 37 : sms * 30 / 37;
     // blocks an SM and row tiles a cluster depend on each other through shared memory: from the
     // most blocks down to what fits
-    for (int occ = blocks_of(K); occ >= 1; --occ) {
+    for (int occ = few_tiles ? 0 : blocks_of(K); occ >= 1; --occ) {
         for (;; c.chunk /= 2) {
             const int chunks = (a.tokens + c.chunk - 1) / c.chunk;
             c.clusters = std::max(1, std::min(P.mt, occ * fit / ck / std::min(chunks, 1 << 20)));
@@ -682,15 +690,23 @@ Cut cut(const Args& a, int ck, int nt, int sms) {
             if (c.max_tiles > 64) c.max_tiles = 64, c.clusters = (P.mt + 63) / 64;
             c.smem = bytes();
             if (occ * (c.smem + 1024) <= 228 * 1024 && c.smem <= limit) {
-                // tiles an SM goes through, and its share of staged activations (from L2)
-                const long long per_sm = ((long long)c.clusters * ck * chunks + sms - 1) / sms;
-                c.ck = ck;
-                c.cost = (double)per_sm * (c.max_tiles * (double)c.slice +
-                                           0.08 * c.slice * c.chunk * token_rows(K) + 4.0);
+                taken();
                 return c;
             }
             if (occ > 1 || c.chunk == 1) break;
         }
+    }
+    for (c.chunk = std::min(a.tokens, tok); few_tiles && c.chunk >= 1; c.chunk /= 2) {
+        c.max_tiles = 0;
+        const size_t fixed = bytes();
+        if (fixed >= limit) continue;
+        c.max_tiles = (int)std::min<size_t>((limit - fixed) / ((size_t)tok * 64), 64);
+        if (c.max_tiles < 1) continue;
+        c.clusters = (P.mt + c.max_tiles - 1) / c.max_tiles;
+        c.max_tiles = (P.mt + c.clusters - 1) / c.clusters;
+        c.smem = bytes();
+        taken();
+        return c;
     }
     return c;
 }
@@ -706,13 +722,16 @@ Cut choose(Args& a, int sms, int& best_nt) {
     a.batch_gq = cols / a.gs, a.batch_gr = cols % a.gs;
     Cut best;
     best_nt = 1;
-    for (int nt = 1; nt <= 4; nt *= 2) {
-        if (nt > 1 && a.tokens <= nt / 2 * tile_tokens(K)) break;
-        for (int ck = 1; ck <= 8 && (ck == 1 || P.kt >= kBatch * ck); ck *= 2) {
-            const Cut c = cut<K>(a, ck, nt, sms);
-            if (c.ck && (!best.ck || c.cost < best.cost)) best = c, best_nt = nt;
+    // Where the sums of a cluster's row tiles never fit beside one token (long rows of fp32 with a
+    // codebook): fewer tiles a cluster, more clusters than fit the GPU at once.
+    for (int few = 0; few < 2 && !best.ck; ++few)
+        for (int nt = 1; nt <= 4; nt *= 2) {
+            if (nt > 1 && a.tokens <= nt / 2 * tile_tokens(K)) break;
+            for (int ck = 1; ck <= 8 && (ck == 1 || P.kt >= kBatch * ck); ck *= 2) {
+                const Cut c = cut<K>(a, ck, nt, sms, few != 0);
+                if (c.ck && (!best.ck || c.cost < best.cost)) best = c, best_nt = nt;
+            }
         }
-    }
     if (!best.ck) return best;
     a.slice = best.slice, a.pitch = best.pitch, a.chunk = best.chunk;
     a.clusters = best.clusters, a.max_tiles = best.max_tiles;
