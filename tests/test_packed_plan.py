@@ -75,3 +75,13 @@ def test_the_longest_rows_are_not_refused(bk, x, book):
                     if m * n < 2 ** 31:
                         _check(bk, m, n, x_dtype=x, group_size=group, book=book, tokens=tokens,
                                x_group_size=32)
+
+
+def test_the_limit_of_a_kernel_is_a_constant():
+    """A kernel's limit on dynamic shared memory is set in one place only, to a constant: a call that
+    set it to its own size could lower it between another thread's call and its launch."""
+    uses = {}
+    for f in sorted(os.listdir(B.CSRC)):
+        text = re.sub(r"//.*", "", open(os.path.join(B.CSRC, f)).read())
+        uses[f] = text.count("cudaFuncAttributeMaxDynamicSharedMemorySize")
+    assert {f: k for f, k in uses.items() if k} == {"common.cuh": 1}

@@ -117,6 +117,15 @@ void count_launches(long long k);
 
 inline int cuda_err(cudaError_t e) { return e == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA; }
 
+// Lets a kernel take BYTES of dynamic shared memory. The limit belongs to the kernel, not to the call:
+// where launches take different amounts, BYTES is the most that any of them takes, so that no thread
+// lowers it between another thread's call and its launch.
+template <size_t BYTES, class Kernel>
+bool allow_smem(Kernel kern) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)BYTES) ==
+           cudaSuccess;
+}
+
 inline bool ws_ok(const void* ws, size_t have, size_t need) {
     return ws != nullptr && have >= need &&
            (reinterpret_cast<uintptr_t>(ws) % kWsAlign) == 0;

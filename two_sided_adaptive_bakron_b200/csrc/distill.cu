@@ -736,12 +736,15 @@ int launch(const X* z, int rows, int V, int64_t ld, const Teacher& T, float* los
     return cuda_err(e);
 }
 
+// What the blocks of an SM share; one block takes less (at most 512 bytes of static arrays beside it).
+constexpr size_t kRowsSmem = 226 * 1024;
+
 template <class X, int DATA>
 int launch_rows(const X* z, int rows, int V, int64_t ld, const Teacher& T, float* loss, float* lse,
                 X* dz, int64_t ldd, int* status, int sms, cudaStream_t st) {
     constexpr int blocks = 1024 / DATA;         // of an SM (1 of 992)
     const size_t lists = (size_t)32 * ((T.k + 3) / 4 * 4) + (size_t)table_slots(T.k) * 4;
-    const size_t room = 226 * 1024 / blocks - 1024 - 512;    // reserved, and the static arrays
+    const size_t room = kRowsSmem / blocks - 1024 - 512;     // reserved, and the static arrays
     const size_t vec = (size_t)DATA * 16;
     size_t keep = room > lists ? (room - lists) / vec : 0;
     keep = std::min({keep, (size_t)16, ((size_t)V / Vec<X>::N + DATA - 1) / DATA});
@@ -749,9 +752,7 @@ int launch_rows(const X* z, int rows, int V, int64_t ld, const Teacher& T, float
     if (keep * DATA < (size_t)V / Vec<X>::N) keep -= keep % 4;
     const size_t smem = keep * vec + lists;
     auto kern = dz ? distill_rows_kernel<X, DATA, true> : distill_rows_kernel<X, DATA, false>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
-        return BAKRON_ERR_CUDA;
+    if (smem > kRowsSmem || !allow_smem<kRowsSmem>(kern)) return BAKRON_ERR_CUDA;
     kern<<<std::min(rows, blocks * sms), DATA + 32, smem, st>>>(z, rows, V, ld, T, loss, lse, dz, ldd,
                                                                 status, (int)keep);
     count_launches(1);

@@ -241,10 +241,7 @@ extern "C" int bakron_ldl(const float* H, int n, float* L, float* D, void* ws, s
     for (int k = 0; k < nsets; ++k)
         w.set[k] = Planes{bufs[4 + 4 * k], bufs[5 + 4 * k], bufs[6 + 4 * k], bufs[7 + 4 * k]};
 
-    if (cudaFuncSetAttribute(ldl_diag::diag_block_kernel,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)ldl_diag::kSmemBytes) != cudaSuccess)
-        return BAKRON_ERR_CUDA;
+    if (!allow_smem<ldl_diag::kSmemBytes>(ldl_diag::diag_block_kernel)) return BAKRON_ERR_CUDA;
     int e;
     // Tensor maps over the outer-block planes (fixed for the whole call).
     CUtensorMap m_xh[2], m_xl[2], m_uh[2], m_ul[2];

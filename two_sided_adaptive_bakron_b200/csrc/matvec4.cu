@@ -621,10 +621,7 @@ matvec4_kernel(const __grid_constant__ Args a) {
 template <int K, int NT, int STEPS>
 int launch(const Args& a, int ck, size_t smem, cudaStream_t st) {
     auto kern = matvec4_kernel<K, NT, STEPS>;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-            cudaSuccess)
-        return BAKRON_ERR_CUDA;
+    if (smem > 48 * 1024 && !allow_smem<kSmemLimit>(kern)) return BAKRON_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.clusters * ck), (unsigned)((a.tokens + a.chunk - 1) / a.chunk));
     cfg.blockDim = dim3(warps_of(K) * 32);

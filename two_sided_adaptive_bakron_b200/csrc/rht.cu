@@ -545,16 +545,20 @@ __global__ void row_scales_kernel(const float* __restrict__ W, int n, int group,
     }
 }
 
+// The row kernel's shared memory: the row and the signs' words.
+constexpr size_t row_smem(int d) {
+    return (size_t)((d + 3) & ~3) * sizeof(float) +
+           (size_t)4 * ((d + 255) / 256) * sizeof(uint64_t);
+}
+constexpr size_t kRowSmem = row_smem(kMaxLen);
+
 template <int U, int OUTER, bool kInverse>
 int launch_rows(const float* X, float* Y, int rows, int d, const uint64_t* signs,
                 const H28f& H, cudaStream_t st) {
     const int T = d / (OUTER * U);
-    const size_t smem = (size_t)((d + 3) & ~3) * sizeof(float) +
-                        (size_t)4 * ((d + 255) / 256) * sizeof(uint64_t);
+    const size_t smem = row_smem(d);
     auto kern = rht_rows_kernel<U, OUTER, kInverse>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
-        return BAKRON_ERR_CUDA;
+    if (!allow_smem<kRowSmem>(kern)) return BAKRON_ERR_CUDA;
     const float scale = 1.0f / sqrtf((float)d);
     kern<<<rows, T < 32 ? 32 : T, smem, st>>>(X, Y, d, T, signs, scale, H);
     count_launches(1);
@@ -566,9 +570,7 @@ int launch_rows28(const float* X, float* Y, int rows, const uint64_t* signs, con
                   cudaStream_t st) {
     constexpr size_t smem = rows28_smem<NQ>();
     auto kern = rht_rows28_kernel<NQ, kInverse>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
-        return BAKRON_ERR_CUDA;
+    if (!allow_smem<smem>(kern)) return BAKRON_ERR_CUDA;
     const float scale = 1.0f / sqrtf((float)(28 * 32 * NQ));
     kern<<<rows, kRows28Threads, smem, st>>>(X, Y, signs, scale, gtab);
     count_launches(1);
@@ -623,9 +625,7 @@ template <bool kInverse, bool kFinal>
 int launch_slab(float* Y, int r, int c, int B, const uint64_t* signs, float scale,
                 cudaStream_t st) {
     auto kern = rht_cols_slab_kernel<kInverse, kFinal>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kSlabSmem) != cudaSuccess)
-        return BAKRON_ERR_CUDA;
+    if (!allow_smem<kSlabSmem>(kern)) return BAKRON_ERR_CUDA;
     kern<<<dim3((c + 31) / 32, (r + kSlabRows - 1) / kSlabRows), kSlabThreads, kSlabSmem, st>>>(
         Y, r, c, B, signs, scale);
     count_launches(1);

@@ -1329,9 +1329,7 @@ int round_impl(const float* Wstar, int m, int n, const float* L_O, const float* 
         if ((e = tc::make_box_map(&lm.rf, Rf, m, n, n, LB))) return e;
     }
 
-    if (cudaFuncSetAttribute(round_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kSmem) != cudaSuccess)
-        return BAKRON_ERR_CUDA;
+    if (!allow_smem<kSmem>(round_kernel)) return BAKRON_ERR_CUDA;
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, round_kernel, NTH, kSmem) !=
             cudaSuccess || per_sm < 1)

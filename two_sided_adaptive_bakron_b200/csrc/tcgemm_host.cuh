@@ -159,9 +159,7 @@ int launch_gemm3x(const CUtensorMap& ah, const CUtensorMap& al, const CUtensorMa
     constexpr size_t smem = gemm_smem_bytes<BN, STAGES>();
     static_assert(smem <= 227 * 1024, "GEMM shared memory above the per-CTA limit");
     auto kern = gemm3x_kernel<BN, STAGES, Epi, CHUNK>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
-        return BAKRON_ERR_CUDA;
+    if (!allow_smem<smem>(kern)) return BAKRON_ERR_CUDA;
     const int nsm = sm_count();
     if (nsm <= 0) return BAKRON_ERR_CUDA;
     int grid = (max_ctas > 0 && max_ctas < nsm) ? max_ctas : nsm;
