@@ -23,17 +23,19 @@ void count_launches(long long k) { __atomic_fetch_add(&g_launches, (unsigned lon
 
 }  // namespace bakron
 
+using namespace bakron;
+
 extern "C" unsigned long long bakron_kernel_launches(void) {
-    return __atomic_load_n(&bakron::g_launches, __ATOMIC_RELAXED);
+    return __atomic_load_n(&g_launches, __ATOMIC_RELAXED);
 }
 
 extern "C" int bakron_read_status(const int* dev_status, void* stream) {
     if (!dev_status) return BAKRON_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int h = 0;
-    if (cudaMemcpyAsync(&h, dev_status, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess)
+    if (!cuda_ok(cudaMemcpyAsync(&h, dev_status, sizeof(int), cudaMemcpyDeviceToHost, st)))
         return BAKRON_ERR_CUDA;
-    if (cudaStreamSynchronize(st) != cudaSuccess) return BAKRON_ERR_CUDA;
+    if (!cuda_ok(cudaStreamSynchronize(st))) return BAKRON_ERR_CUDA;
     return h;
 }
 

@@ -115,15 +115,22 @@ uint64_t spin_limit_ns();
 // Counts the kernels this library has launched in this process (diagnostics).
 void count_launches(long long k);
 
-inline int cuda_err(cudaError_t e) { return e == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA; }
+// A call that failed is reported once: the runtime keeps its error for the next cudaGetLastError, where
+// a later launch that succeeded would answer for it. (Errors that have ended the context stay.)
+inline bool cuda_ok(cudaError_t e) {
+    if (e == cudaSuccess) return true;
+    (void)cudaGetLastError();
+    return false;
+}
+inline int cuda_err(cudaError_t e) { return cuda_ok(e) ? BAKRON_OK : BAKRON_ERR_CUDA; }
 
 // Lets a kernel take BYTES of dynamic shared memory. The limit belongs to the kernel, not to the call:
 // where launches take different amounts, BYTES is the most that any of them takes, so that no thread
 // lowers it between another thread's call and its launch.
 template <size_t BYTES, class Kernel>
 bool allow_smem(Kernel kern) {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)BYTES) ==
-           cudaSuccess;
+    return cuda_ok(
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)BYTES));
 }
 
 inline bool ws_ok(const void* ws, size_t have, size_t need) {

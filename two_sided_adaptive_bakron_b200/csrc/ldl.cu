@@ -182,14 +182,14 @@ std::atomic<unsigned> g_side_next{0};
 // Two distinct side streams of the current device's pool.
 int side_streams(cudaStream_t* a, cudaStream_t* b) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+    if (!cuda_ok(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices)
         return BAKRON_ERR_CUDA;
     const unsigned k = g_side_next.fetch_add(2, std::memory_order_relaxed) % kSidePool;
     std::lock_guard<std::mutex> lock(g_side_mu);
     cudaStream_t* out[2] = {a, b};
     for (unsigned i = 0; i < 2; ++i) {
         cudaStream_t& s = g_side[dev][(k + i) % kSidePool];
-        if (!s && cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) != cudaSuccess) {
+        if (!s && !cuda_ok(cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking))) {
             s = nullptr;
             return BAKRON_ERR_CUDA;
         }
@@ -209,7 +209,7 @@ struct CallEvents {
     }
     int make() {
         for (n = 0; n < kCount; ++n)
-            if (cudaEventCreateWithFlags(&ev[n], cudaEventDisableTiming) != cudaSuccess)
+            if (!cuda_ok(cudaEventCreateWithFlags(&ev[n], cudaEventDisableTiming)))
                 return BAKRON_ERR_CUDA;
         return BAKRON_OK;
     }

@@ -51,11 +51,11 @@ unsigned long long current_ctx_id() {
     std::call_once(once, [] {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) ==
-                cudaSuccess && q == cudaDriverEntryPointSuccess)
+        if (cuda_ok(cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q)) &&
+            q == cudaDriverEntryPointSuccess)
             get_cur = reinterpret_cast<CtxGetCurrentFn>(p);
         p = nullptr;
-        if (cudaGetDriverEntryPoint("cuCtxGetId", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        if (cuda_ok(cudaGetDriverEntryPoint("cuCtxGetId", &p, cudaEnableDefault, &q)) &&
             q == cudaDriverEntryPointSuccess)
             get_id = reinterpret_cast<CtxGetIdFn>(p);
     });
@@ -71,7 +71,7 @@ unsigned long long current_ctx_id() {
 // the first call in that context, never while `stream` is capturing).
 int scratch_address(cudaStream_t stream, void** out) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+    if (!cuda_ok(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices)
         return BAKRON_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_mu);
     const unsigned long long id = current_ctx_id();
@@ -80,10 +80,10 @@ int scratch_address(cudaStream_t stream, void** out) {
         return BAKRON_OK;
     }
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return BAKRON_ERR_CUDA;
+    if (!cuda_ok(cudaStreamIsCapturing(stream, &cap))) return BAKRON_ERR_CUDA;
     if (cap != cudaStreamCaptureStatusNone) return BAKRON_ERR_CAPTURE;
     void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_ldl_scratch) != cudaSuccess || !p) return BAKRON_ERR_CUDA;
+    if (!cuda_ok(cudaGetSymbolAddress(&p, g_ldl_scratch)) || !p) return BAKRON_ERR_CUDA;
     const unsigned long long id_now = current_ctx_id();   // the lookup made a context current
     g_addr[dev] = CachedAddr{id_now, id_now ? p : nullptr};
     *out = p;

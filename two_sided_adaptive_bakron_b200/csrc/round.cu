@@ -1331,8 +1331,8 @@ int round_impl(const float* Wstar, int m, int n, const float* L_O, const float* 
 
     if (!allow_smem<kSmem>(round_kernel)) return BAKRON_ERR_CUDA;
     int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, round_kernel, NTH, kSmem) !=
-            cudaSuccess || per_sm < 1)
+    if (!cuda_ok(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, round_kernel, NTH, kSmem)) ||
+        per_sm < 1)
         return BAKRON_ERR_CUDA;
     const int resident = per_sm * tc::sm_count();
     if (resident < 2) return BAKRON_ERR_CUDA;

@@ -14,8 +14,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     std::call_once(once, [] {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-                cudaSuccess &&
+        if (cuda_ok(cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q)) &&
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
     });
@@ -61,15 +60,15 @@ int sm_count() {
     static std::mutex mu;
     static int cached[64] = {0};
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+    if (!cuda_ok(cudaGetDevice(&dev)) || dev < 0) return 0;
     if (dev >= 64) {
         int v = 0;
-        return cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? v : 0;
+        return cuda_ok(cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev)) ? v : 0;
     }
     std::lock_guard<std::mutex> lock(mu);
     if (cached[dev] == 0) {
         int v = 0;
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        if (!cuda_ok(cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev))) return 0;
         cached[dev] = v;
     }
     return cached[dev];
