@@ -119,3 +119,46 @@ def test_binding_refuses_what_the_library_cannot_see(bk):
     meta = torch.zeros(4, 64, device="meta")
     with pytest.raises(ValueError, match="CUDA"):
         bk._rows(meta, "x", meta.get_device())
+
+
+class _Stream:
+    def __init__(self, device, cuda_stream=7):
+        self.device, self.cuda_stream = torch.device(device), cuda_stream
+
+
+def test_a_stream_handle_is_one_of_the_tensors_device(bk, monkeypatch):
+    """Not of the current device, which may be another."""
+    made = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream",
+                        lambda h, device=None: made.append((h, device)) or _Stream(device, h))
+    monkeypatch.setattr(torch.cuda, "default_stream",
+                        lambda device=None: made.append((0, device)) or _Stream(device, 0))
+    dev = torch.device("cuda:1")
+    for handle in (0x70, 0):
+        assert bk._stream_on(handle, dev).device == dev
+    assert made == [(0x70, dev), (0, dev)]
+    own = _Stream("cuda:1")
+    assert bk._stream_on(own, dev) is own
+    with pytest.raises(ValueError, match="cuda:1"):
+        bk._stream_on(_Stream("cuda:0"), dev)
+
+
+def test_calls_take_the_device_of_their_tensors(bk, monkeypatch):
+    seen = []
+
+    class Enough(Exception):
+        pass
+
+    def stop(stream, device):
+        seen.append((stream, device))
+        raise Enough
+    monkeypatch.setattr(bk, "_stream_on", stop)
+    t = torch.zeros(4, 64, device="meta")
+    for call in [lambda: bk.pack4(t, t, stream=5), lambda: bk.unpack4(t, 4, 64, stream=5),
+                 lambda: bk.matvec4(t, 4, 64, t, stream=5), lambda: bk.rms_norm_q8(t, stream=5),
+                 lambda: bk.distill(t, t, t, stream=5), lambda: bk.rms_norm_q8(x=t, stream=5)]:
+        with pytest.raises(Enough):
+            call()
+    assert seen == [(5, t.device)] * 6
+    with pytest.raises(ValueError, match="tensors"):
+        bk.rms_norm_q8([1.0], stream=5)

@@ -687,17 +687,29 @@ def proxy_loss(dW, H_O, H_I, stream=None) -> torch.Tensor:
     return loss
 
 
+def _stream_on(stream, device):
+    """The torch stream of ``device`` that a Stream object or an integer handle names."""
+    if hasattr(stream, "cuda_stream"):
+        if device.type == "cuda" and stream.device != device:
+            raise ValueError(f"stream: expected one of {device}, got one of {stream.device}")
+        return stream
+    if int(stream):
+        return torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.default_stream(device)
+
+
 def _on_stream(f):
     """Runs a call that is given a ``stream`` with that stream current: what it allocates then
-    belongs to the stream that writes it, and nothing the current stream still uses is reused."""
+    belongs to the stream that writes it, and nothing the current stream still uses is reused. A
+    handle is one of the device that the call's first tensor is on."""
     @functools.wraps(f)
     def call(*args, stream=None, **kw):
         if stream is None:
             return f(*args, **kw)
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else \
-                torch.cuda.default_stream()
-        with torch.cuda.stream(stream):
+        first = next((t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)), None)
+        if first is None:
+            raise ValueError("expected tensors")
+        with torch.cuda.stream(_stream_on(stream, first.device)):
             return f(*args, **kw)
     return call
 
