@@ -331,7 +331,7 @@ int bakron_unpack4(const void* packed, int m, int n, int group_size, int unsigne
  * v(code) is the code itself or, with a codebook, its entry. 8-bit activations stand for
  * x_scales[t][j / x_group_size] * x[t][j]. Products are exact or carried to 22 bits and more
  * (fp32 activations: 24 bits; with a codebook: entries to 22 bits for fp16 and 8-bit
- * activations, 16 for bf16, 24 for fp32), sums are fp32 (8-bit activations on the integer grid:
+ * activations, 24 for fp32, for bf16 24 with an fp32 result and 16 with a 16-bit one), sums are fp32 (8-bit activations on the integer grid:
  * exact within 64 columns), and the result is rounded once to y's type.
  * Any number of tokens is right; the weights are read once for up to 32 tokens (8 tokens of fp32;
  * fewer in layers of very long rows), so it is meant for few.

@@ -550,3 +550,25 @@ def test_product_of_the_longest_rows_of_many_tiles(bk, m, n, tokens):
     ref, a = xt.double() @ W.T, xt.double().abs() @ W.abs().T
     tol = 2.0 ** -24 * ref.abs() + a * (2.0 ** -23 + (n / 64 + 24) * 2.0 ** -23)
     assert ((got.double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("m,n,group,tokens", [(17, 70, 32, 1), (130, 520, 64, 8), (1003, 2500, None, 3),
+                                              (100, 1000, 96, 17), (256, 4096, 128, 33),
+                                              (20, 65536, 32, 9)])
+@pytest.mark.parametrize("book", [BOOK16, [v * 1.0e-20 for v in BOOK16], [-1.1, 0.7]])
+def test_fp32_results_of_bf16_activations_keep_the_entries(bk, m, n, group, tokens, book):
+    """Codebook entries of 24 bits, as with fp32 activations (carry 2^-23), not the 16 that a 16-bit
+    result is given."""
+    codes, scales = _layer(m, n, group, m, book)
+    x = torch.randn(tokens, n, device="cuda").bfloat16()
+    got = bk.PackedLayer(_cuda(codes), _cuda(scales), group, book).matvec(x, out_dtype=torch.float32)
+    ref, a = matvec4(codes, scales, x.double().cpu().numpy(), group, book)
+    tol = HALF[torch.float32] * np.abs(ref) + a * (2.0 ** -23 + (n / 64 + 24) * 2.0 ** -23)
+    err = np.abs(got.double().cpu().numpy() - ref)
+    assert (err <= tol).all(), float((err / np.maximum(tol, 1e-300)).max())
+    # one column: the entry itself, times a power of two
+    one = np.arange(len(book), dtype=np.int8)[:, None]
+    got = bk.PackedLayer(_cuda(one), torch.ones(len(book), device="cuda"), None, book).matvec(
+        torch.full((1, 1), 0.5, device="cuda").bfloat16(), out_dtype=torch.float32)
+    want = torch.tensor(book, device="cuda") * 0.5
+    assert ((got[0] - want).abs() <= 2.0 ** -23 * want.abs()).all()

@@ -85,3 +85,13 @@ def test_the_limit_of_a_kernel_is_a_constant():
         text = re.sub(r"//.*", "", open(os.path.join(B.CSRC, f)).read())
         uses[f] = text.count("cudaFuncAttributeMaxDynamicSharedMemorySize")
     assert {f: k for f, k in uses.items() if k} == {"common.cuh": 1}
+
+
+def test_plans_of_fp32_results_of_bf16_activations(bk):
+    """With a codebook they take a table of three parts."""
+    for m, n, group, tokens in [(28672, 8192, None, 16), (14336, 4096, None, 17), (5120, 13824, 128, 32),
+                                (4096, 65536, 32, 40), (20, 65536, 32, 9), (1, 1, None, 1),
+                                (70000, 8960, 64, 33)]:
+        p = _check(bk, m, n, x_dtype=torch.bfloat16, group_size=group, book=True, tokens=tokens,
+                   out_dtype=torch.float32)
+        assert p["smem"] > 3 * 32768

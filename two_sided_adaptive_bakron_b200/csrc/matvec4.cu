@@ -23,7 +23,8 @@
 //     stand in three columns of the tensor tile, so their products are exact too.
 //   * Codebook entries come in pairs from a table in shared memory that is indexed by a byte of two
 //     codes and has one copy a lane (bank), so the reads never conflict; an entry is held as two
-//     16-bit parts (fp32 activations: three), each multiplied on its own.
+//     16-bit parts (three for fp32 activations, and for bf16 ones with an fp32 result), each multiplied
+//     on its own.
 //   * Products are summed over 64 (32) columns in the tensor core's fp32 (int8: exactly, in int32),
 //     then scaled and added in fp32 round-to-nearest.
 //   * A cluster's blocks take slices of the columns for the same rows and add their sums through
@@ -52,9 +53,10 @@ constexpr int kStages = 2;
 // dynamic part.
 constexpr size_t kSmemLimit = 227 * 1024;
 
-enum Kind { kF16, kBf16, kF32, kI8, kF16Book, kBf16Book, kF32Book };
+// kBf16Wide: bf16 activations with a codebook and an fp32 result, which would show entries of 16 bits.
+enum Kind { kF16, kBf16, kF32, kI8, kF16Book, kBf16Book, kBf16Wide, kF32Book };
 constexpr bool is_book(int k) { return k >= kF16Book; }
-constexpr int planes(int k) { return k == kF32Book ? 3 : 2; }
+constexpr int planes(int k) { return k >= kBf16Wide ? 3 : 2; }
 constexpr bool is_split(int k) { return k == kF32 || k == kF32Book; }   // fp32 activations
 constexpr bool is_half(int k) { return k == kF16 || k == kF16Book; }
 // tokens in one 8-column tile of the product, staged rows a token
@@ -296,7 +298,7 @@ matvec4_kernel(const __grid_constant__ Args a) {
     float* sxs = reinterpret_cast<float*>(head_tile + kWarps);   // [kTok][steps of x in the slice]
     const int xg0 = a.Gx > 1 ? kt0 * 64 / a.gx : 0;
 
-    if constexpr (K == kF32 || K == kF32Book) {
+    if constexpr (is_split(K)) {
         stage_x<K, kThreads, float>(sx, a, t0, count, kt0 * 64, batches * kBatch);
     } else if constexpr (K == kF16) {
         stage_x<K, kThreads, __half>(sx, a, t0, count, kt0 * 64, batches * kBatch);
@@ -779,7 +781,7 @@ float cut16(float f) {       // its upper 16 bits: a bf16, rounded toward zero
 
 // The 16-bit parts of the entries. f16: the entries are first brought to [2^13, 2^14) by a power
 // of two (out1, out2 undo it), then a part is the rounding of what is left: 22 bits and more of
-// the largest. bf16: upper bits, then the rounding of what is left: 16 bits; fp32 takes three parts.
+// the largest. bf16: upper bits, then the rounding of what is left: 16 bits, or 24 in three parts.
 template <int K>
 void split_book(const float* c, int entries, Args& a) {
     std::memset(&a.book, 0, sizeof a.book);
@@ -835,6 +837,8 @@ template <class F>
 int with_kind(const Args& a, bool book, F f) {
     if (book) {
         if (a.x_dtype == BAKRON_F32) return f(std::integral_constant<int, kF32Book>());
+        if (a.x_dtype == BAKRON_BF16 && a.y_dtype == BAKRON_F32)
+            return f(std::integral_constant<int, kBf16Wide>());
         if (a.x_dtype == BAKRON_BF16) return f(std::integral_constant<int, kBf16Book>());
         return f(std::integral_constant<int, kF16Book>());
     }
