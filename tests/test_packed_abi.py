@@ -162,3 +162,19 @@ def test_calls_take_the_device_of_their_tensors(bk, monkeypatch):
     assert seen == [(5, t.device)] * 6
     with pytest.raises(ValueError, match="tensors"):
         bk.rms_norm_q8([1.0], stream=5)
+
+
+def test_an_input_that_needs_a_gradient_is_refused(bk):
+    """matvec4 and rms_norm_q8 have no gradient: they do not drop one in silence."""
+    x = torch.zeros(4, 64, requires_grad=True)
+    packed = torch.zeros(bk.bakron_pack4_bytes(4, 64, 64), dtype=torch.uint8)
+    calls = [lambda: bk.matvec4(packed, 4, 64, x), lambda: bk.rms_norm_q8(x),
+             lambda: bk.rms_norm_q8(x.detach(), residual=x),
+             lambda: bk.matvec4(packed, 4, 64, x.detach().to(torch.int8), x_scales=x[:, :1])]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    with torch.no_grad():
+        for call in calls:
+            with pytest.raises(ValueError, match="CUDA"):    # host tensors: refused further on
+                call()

@@ -714,6 +714,14 @@ def _on_stream(f):
     return call
 
 
+def _no_gradient(where: str):
+    """The library has no gradient of these calls: an input that needs one is refused, where a result
+    without history would drop it in silence."""
+    if torch.is_grad_enabled():
+        raise ValueError(f"{where}: an input requires a gradient, which this call does not pass on; call "
+                         "it under torch.no_grad() or with detached inputs")
+
+
 def _status_of(status, device, check: bool):
     """(status word, whether to read it): the caller's own word is left to the caller."""
     if status is not None:
@@ -755,7 +763,10 @@ def unpack4(packed, m: int, n: int, group_size=None, unsigned: bool = False):
 def matvec4(packed, m: int, n: int, x, group_size=None, codebook=None, x_scales=None,
             x_group_size=None, out_dtype=None) -> torch.Tensor:
     """y = x W^T for a layer (m x n) in the 4-bit layout and x of one token (n) or a few (tokens x
-    n); y has x's type (float32 for int8 x) unless ``out_dtype`` names another."""
+    n); y has x's type (float32 for int8 x) unless ``out_dtype`` names another. It has no gradient:
+    an x that requires one is refused while gradients are recorded."""
+    if x.requires_grad or (x_scales is not None and x_scales.requires_grad):
+        _no_gradient("matvec4")
     shape = x.shape
     if shape[-1] != n:
         raise ValueError(f"x: expected {n} columns, got {tuple(shape)}")
@@ -775,7 +786,10 @@ def rms_norm_q8(x, weight=None, eps: float = 1e-6, residual=None, group_size=Non
     """(q int8, scales, sum): the norm of x + residual in 8 bits, and the sum in x's type (None
     without a residual, unless ``sum_out`` asks for it). Scales: one per row, or rows x G with a
     group size. Rows that are not finite give NaN scales and, where the caller gives a ``status``
-    word, BAKRON_ERR_NONFINITE in it."""
+    word, BAKRON_ERR_NONFINITE in it. It has no gradient: an x or residual that requires one is
+    refused while gradients are recorded (``weight`` is taken as a constant)."""
+    if x.requires_grad or (residual is not None and residual.requires_grad):
+        _no_gradient("rms_norm_q8")
     shape = x.shape
     n = shape[-1]
     _, G = _steps(n, group_size)
