@@ -572,3 +572,28 @@ def test_fp32_results_of_bf16_activations_keep_the_entries(bk, m, n, group, toke
         torch.full((1, 1), 0.5, device="cuda").bfloat16(), out_dtype=torch.float32)
     want = torch.tensor(book, device="cuda") * 0.5
     assert ((got[0] - want).abs() <= 2.0 ** -23 * want.abs()).all()
+
+
+def test_transposed_steps_and_lists_are_refused(bk):
+    """Contiguous tensors of the right length that stand the other way round."""
+    m, n, G = 48, 256, 8
+    codes, steps = torch.zeros(m, n, dtype=torch.int8, device="cuda"), torch.rand(m, G, device="cuda")
+    layer = bk.PackedLayer(codes, steps, 32)
+    with pytest.raises(ValueError, match="48 x 8"):
+        bk.PackedLayer(codes, steps.T.contiguous(), 32)
+    out = torch.empty(G, m, device="cuda")
+    with pytest.raises(ValueError, match="48 x 8"):
+        bk.bakron_unpack4(layer.packed, 32, False, codes, out)
+    q, xs, _ = bk.rms_norm_q8(torch.randn(3, n, device="cuda"), group_size=32)
+    with pytest.raises(ValueError, match="3 x 8"):
+        layer.matvec(q, xs.T.contiguous(), 32)
+    y = layer.matvec(q, xs, 32)
+    assert torch.equal(layer.matvec(q, xs.view(-1), 32), y)          # flat ones as before
+    assert torch.equal(layer.matvec(q[:1], xs[0], 32), y[:1])
+    z = torch.randn(5, 40, device="cuda")
+    top, idx = z.topk(3, dim=1)
+    ref = bk.distill(z, idx, top)
+    for i, t in [(idx, top.T.contiguous()), (idx.T.contiguous(), top)]:
+        with pytest.raises(ValueError):
+            bk.distill(z, i, t)
+    assert torch.equal(bk.distill(z, idx, top.view(-1))[0], ref[0])

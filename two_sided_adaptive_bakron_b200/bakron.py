@@ -321,6 +321,13 @@ def _flat(t, dtype, numel: int, name: str, device: int) -> int:
     return t.data_ptr()
 
 
+def _grid(t, dtype, rows: int, cols: int, name: str, device: int) -> int:
+    """The same for rows x cols elements: neither a transposed tensor nor rows cut otherwise."""
+    if t.dim() > 1 and rows > 1 and cols > 1 and t.shape[0] != rows and t.shape[-1] != cols:
+        raise ValueError(f"{name}: expected {rows} x {cols}, got {tuple(t.shape)}")
+    return _flat(t, dtype, rows * cols, name, device)
+
+
 def _dtype(t: torch.Tensor, name: str) -> int:
     d = _DTYPES.get(t.dtype)
     if d is None:
@@ -391,7 +398,7 @@ def bakron_pack4(codes, scales, group_size, unsigned_codes, packed, dev_status,
         raise ValueError(f"codes: expected torch.int8, got {codes.dtype}")
     g, G = _steps(n, group_size)
     return _call(lib().bakron_pack4, dev, stream, codes.data_ptr(), ldc,
-                 _flat(scales, torch.float32, m * G, "scales", dev), m, n, g,
+                 _grid(scales, torch.float32, m, G, "scales", dev), m, n, g,
                  int(bool(unsigned_codes)),
                  _flat(packed, torch.uint8, _packed_bytes(m, n, G), "packed", dev),
                  _flat(dev_status, torch.int32, 1, "dev_status", dev))
@@ -406,7 +413,7 @@ def bakron_unpack4(packed, group_size, unsigned_codes, codes, scales, stream=Non
     return _call(lib().bakron_unpack4, dev, stream,
                  _flat(packed, torch.uint8, _packed_bytes(m, n, G), "packed", dev), m, n, g,
                  int(bool(unsigned_codes)), codes.data_ptr(), ldc,
-                 _flat(scales, torch.float32, m * G, "scales", dev))
+                 _grid(scales, torch.float32, m, G, "scales", dev))
 
 
 def bakron_matvec4(packed, group_size, codebook, x, x_scales, x_group_size, y,
@@ -428,7 +435,7 @@ def _matvec4(packed, m, group_size, codebook, x, x_scales, x_group_size, y, ldy,
     gx, xs = n, None
     if x_scales is not None:
         gx, Gx = _steps(n, x_group_size)
-        xs = _flat(x_scales, torch.float32, tokens * Gx, "x_scales", dev)
+        xs = _grid(x_scales, torch.float32, tokens, Gx, "x_scales", dev)
     return _call(lib().bakron_matvec4, dev, stream,
                  _flat(packed, torch.uint8, _packed_bytes(m, n, G), "packed", dev), m, n, g, cb,
                  bits, x.data_ptr(), _dtype(x, "x"), ldx, xs, gx, tokens, y.data_ptr(),
@@ -445,8 +452,8 @@ def bakron_rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out=
         sr, sn, lds = _rows(sum_out, "sum_out", dev)
         if sr != rows or sn != n or sum_out.dtype != x.dtype:
             raise ValueError("sum_out: expected the shape and type of x")
-    _flat(q, torch.int8, rows * n, "q", dev)
-    _flat(scales, torch.float32, rows * G, "scales", dev)
+    _grid(q, torch.int8, rows, n, "q", dev)
+    _grid(scales, torch.float32, rows, G, "scales", dev)
     return _rms_norm_q8(x, residual, weight, eps, group_size, q, scales, sum_out, lds, dev_status,
                         dev, stream)
 
@@ -495,9 +502,9 @@ def _distill(logits, top_idx, top_logits, teacher_lse, row_weights, temperature,
     rows, V, ld = _rows(logits, "logits", dev)
     k = top_idx.shape[-1]
     return _call(lib().bakron_distill, dev, stream, logits.data_ptr(), _dtype(logits, "logits"),
-                 rows, V, ld, _flat(top_idx, top_idx.dtype, rows * k, "top_idx", dev),
+                 rows, V, ld, _grid(top_idx, top_idx.dtype, rows, k, "top_idx", dev),
                  _dtype(top_idx, "top_idx"),
-                 _flat(top_logits, top_logits.dtype, rows * k, "top_logits", dev),
+                 _grid(top_logits, top_logits.dtype, rows, k, "top_logits", dev),
                  _dtype(top_logits, "top_logits"), k,
                  None if teacher_lse is None else
                  _flat(teacher_lse, torch.float32, rows, "teacher_lse", dev),
