@@ -178,3 +178,16 @@ def test_an_input_that_needs_a_gradient_is_refused(bk):
         for call in calls:
             with pytest.raises(ValueError, match="CUDA"):    # host tensors: refused further on
                 call()
+
+
+def test_norm_in_place_takes_the_stride_of_its_input(L):
+    """A sum in the buffer of x or of the residual, but with other rows: refused, for a row would be
+    written while another one is read there."""
+    far = ctypes.c_void_p(0x9000)
+
+    def nq(x=P, ldx=64, r=far, ldr=64, sm=P, lds=64, rows=2):
+        return L.bakron_rms_norm_q8(x, ldx, r, ldr, 2, None, 0, rows, 64, 1e-6, 32, far, far, sm, lds,
+                                    None, None)
+    for bad in [dict(lds=72), dict(ldx=72), dict(sm=far, lds=72), dict(sm=far, ldr=80),
+                dict(r=None, lds=65)]:
+        assert nq(**bad) == INVALID, bad

@@ -497,7 +497,8 @@ extern "C" int bakron_rms_norm_q8(const void* x, int64_t ldx, const void* residu
                                   void* sum, int64_t lds, int* dev_status, void* stream) {
     if (!float_dtype(dtype) || (weight && !float_dtype(weight_dtype)) || rows < 0 || n < 1 ||
         n > 65536 || !(eps > 0.f) || !std::isfinite(eps) || !group_ok(group_size, n) ||
-        ldx < n || (residual && ldr < n) || (sum && lds < n))
+        ldx < n || (residual && ldr < n) || (sum && lds < n) ||
+        (rows > 1 && sum && ((sum == x && lds != ldx) || (sum == residual && lds != ldr))))
         return BAKRON_ERR_INVALID_ARG;
     if (rows == 0) return BAKRON_OK;
     const size_t b = dtype_bytes(dtype);
