@@ -95,3 +95,9 @@ def test_plans_of_fp32_results_of_bf16_activations(bk):
         p = _check(bk, m, n, x_dtype=torch.bfloat16, group_size=group, book=True, tokens=tokens,
                    out_dtype=torch.float32)
         assert p["smem"] > 3 * 32768
+
+
+def test_the_number_of_sms_is_asked():
+    for f in sorted(os.listdir(B.CSRC)):
+        text = re.sub(r"//.*", "", open(os.path.join(B.CSRC, f)).read())
+        assert not re.search(r"\b148\b", text), f

@@ -24,6 +24,7 @@
 #include <cmath>
 
 #include "lowp.cuh"
+#include "tcgemm_host.cuh"
 
 namespace bakron {
 namespace {
@@ -455,13 +456,13 @@ int launch_groups(const Args& a, int rows, cudaStream_t st) {
 // blocks stay small, two where they are 16-bit values (fp32 takes twice the registers), nothing kept
 // above 1024 threads' worth.
 template <class X, bool WIDE>
-int plan(const Args& a, int rows, cudaStream_t st) {
+int plan(const Args& a, int rows, int sms, cudaStream_t st) {
     constexpr bool half = sizeof(X) == 2;
     const int chunks = (a.n + 7) / 8;
     if (a.G > 1 && 256 % a.gs == 0) {
         // many rows: long rounds of small blocks; few rows: as many threads as help one row
         if (chunks <= 64) return launch_groups<X, 64, WIDE>(a, rows, st);
-        if (chunks <= 128 || rows >= 4 * 148) return launch_groups<X, 128, WIDE>(a, rows, st);
+        if (chunks <= 128 || rows >= 4 * sms) return launch_groups<X, 128, WIDE>(a, rows, st);
         return launch_groups<X, 512, WIDE>(a, rows, st);
     }
     if (chunks <= 64) return launch<X, 1, 64, WIDE>(a, rows, st);
@@ -483,7 +484,9 @@ int plan(const Args& a, int rows, cudaStream_t st) {
     using X = typename Elem<D>::T;
     const bool wide = a.n % 8 == 0 && a.wide_x && (!a.r || a.wide_r) && a.wide_w && a.same_w &&
                       (!a.sum || a.wide_sum) && a.wide_q;
-    return wide ? plan<X, true>(a, rows, st) : plan<X, false>(a, rows, st);
+    const int sms = tc::sm_count();
+    if (sms <= 0) return BAKRON_ERR_CUDA;
+    return wide ? plan<X, true>(a, rows, sms, st) : plan<X, false>(a, rows, sms, st);
 }
 
 }  // namespace
