@@ -390,3 +390,51 @@ def test_drawn_cases(bk, seed):
         w = torch.from_numpy(rng.standard_normal(rows).astype(np.float32)).cuda()
         w[rows // 2] = 0
     _check(bk, z, idx.to(torch.int32) if seed % 3 else idx, top, tau, mass, w, dt=dt)
+
+
+class _Rows:
+    """Stands for the library in ``_check``: the given rows of one call over many."""
+
+    def __init__(self, out, rows):
+        self.out, self.rows = out, rows
+
+    def distill(self, z, idx, top, tau, mass, w, grad=True, dlogits=None):
+        loss, lse, dz = self.out
+        return loss[self.rows], lse[self.rows], None if dz is None else dz[self.rows]
+
+
+# V: rows for blocks of 128, 512 and 992 threads, which keep them whole, in part, or hardly at all
+@pytest.mark.parametrize("dt,V,k", [("f32", 9, 3), ("bf16", 777, 32), ("f16", 12001, 40),
+                                    ("f32", 32000, 20), ("bf16", 100003, 64), ("bf16", 131072, 64),
+                                    ("f32", 100000, 33), ("f16", 200001, 7), ("bf16", 270000, 1024)])
+@pytest.mark.parametrize("form", ["plain", "mass", "shifted", "in place", "repeats"])
+def test_many_rows_against_the_oracle(bk, dt, V, k, form):
+    """Rows from the whole of one call over many, each against the oracle under the bounds of a call
+    of few: with the teacher's own log-sum-exp, with an output whose rows lie otherwise to 16-byte
+    boundaries than the logits' (and apart by another stride), in place, and with indices that stand
+    in a list more than once."""
+    rows, tau = 611, [1.0, 1.5][k % 2]
+    z, idx, top, teacher = _problem(rows, V, k, dt, V + len(form), repeat=form == "repeats" and V > 9)
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    w = torch.randn(rows, generator=gen, device="cuda")
+    w[torch.rand(rows, generator=gen, device="cuda") < 0.2] = 0
+    mass = torch.logsumexp(teacher.double() / tau, dim=1).float() if form == "mass" else None
+    del teacher
+    pick = torch.tensor([0, 1, 147, 295, 296, 592, 609, 610], device="cuda")
+    zr, ir, tr, wr = z[pick], idx[pick], top[pick], w[pick]
+    mr = None if mass is None else mass[pick]
+    st = bk.new_status("cuda")
+    dlogits = around = None
+    if form == "shifted":
+        around = torch.full((rows, V + 13), 9.0, device="cuda").to(DT[dt])
+        dlogits = around[:, 5:5 + V]
+    elif form == "in place":
+        dlogits = z
+    alone = bk.distill(z, idx, top, tau, mass, w, grad=False, status=st)
+    out = bk.distill(z, idx, top, tau, mass, w, dlogits=dlogits, status=st)
+    _check(_Rows(out, pick), zr, ir, tr, tau, mr, wr, dt=dt)
+    _check(_Rows(alone, pick), zr, ir, tr, tau, mr, wr, grad=False, dt=dt)
+    assert bk.bakron_read_status(st) == 0
+    assert not out[2][w == 0].any() and not out[0][w == 0].any()
+    if around is not None:
+        assert (around[:, :5] == 9).all() and (around[:, 5 + V:] == 9).all()
