@@ -49,9 +49,8 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kStages = 2;
-// Shared memory of a block, static arrays included: the kernel has none, all of it is laid out in the
-// dynamic part.
-constexpr size_t kSmemLimit = 227 * 1024;
+// Shared memory of a block: static arrays (128 bytes at most) and the dynamic part together.
+constexpr size_t kSmemLimit = 227 * 1024, kStaticSmem = 128;
 
 // kBf16Wide: bf16 activations with a codebook and an fp32 result, which would show entries of 16 bits.
 enum Kind { kF16, kBf16, kF32, kI8, kF16Book, kBf16Book, kBf16Wide, kF32Book };
@@ -271,6 +270,7 @@ matvec4_kernel(const __grid_constant__ Args a) {
     constexpr bool HALF = STEPS == kAnywhere;
     constexpr int kWarps = warps_of(K), kThreads = kWarps * 32;
     extern __shared__ __align__(128) char smem[];
+    __shared__ int head_tile[kWarps];      // the tile that a warp ends but did not begin, or -1
     cg::cluster_group cluster = cg::this_cluster();
     const int ck = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int lane = threadIdx.x & 31, g = lane / 4, t = lane % 4;
@@ -292,10 +292,9 @@ matvec4_kernel(const __grid_constant__ Args a) {
     if constexpr (is_book(K)) at += planes(K) * 32768;
     const int rows = a.max_tiles * 16;
     float* part = reinterpret_cast<float*>(at);           // [kTok][rows]
-    float* head = part + kTok * rows;                     // [warp - 1][kTok][16]
-    int* head_tile = reinterpret_cast<int*>(head + (kWarps - 1) * kTok * 16);   // the tile that a
-                                                          // warp ends but did not begin (or -1)
-    float* sxs = reinterpret_cast<float*>(head_tile + kWarps);   // [kTok][steps of x in the slice]
+    // [warp][kTok][16], without a place for the first warp, which begins all of its tiles
+    float* head = part + kTok * (rows - 16);
+    float* sxs = head + kWarps * kTok * 16;               // [kTok][steps of x in the slice]
     const int xg0 = a.Gx > 1 ? kt0 * 64 / a.gx : 0;
 
     if constexpr (is_split(K)) {
@@ -550,8 +549,8 @@ matvec4_kernel(const __grid_constant__ Args a) {
         }
         if (++c_batch == batches || unit + 1 == u1) {
             // the tile's sums: whole tiles and a tile's first part to its rows, the end of a tile
-            // that another warp began to this warp's place (the first warp begins all of its own)
-            float* out = whole ? part + (c_tile - rt0) * 16 : head + (warp - 1) * kTok * 16;
+            // that another warp began to this warp's place
+            float* out = whole ? part + (c_tile - rt0) * 16 : head + warp * kTok * 16;
             const int ld = whole ? rows : 16;
 #pragma unroll
             for (int q = 0; q < NT; ++q) {
@@ -581,7 +580,7 @@ matvec4_kernel(const __grid_constant__ Args a) {
         const int tile = head_tile[w];
         if (tile < 0) continue;
         for (int e = threadIdx.x; e < kTok * 16; e += kThreads)
-            part[(e / 16) * rows + tile * 16 + e % 16] += head[(w - 1) * kTok * 16 + e];
+            part[(e / 16) * rows + tile * 16 + e % 16] += head[w * kTok * 16 + e];
     }
 
     // the blocks of the cluster add up a share of the rows each, four rows a thread
@@ -623,7 +622,7 @@ matvec4_kernel(const __grid_constant__ Args a) {
 template <int K, int NT, int STEPS>
 int launch(const Args& a, int ck, size_t smem, cudaStream_t st) {
     auto kern = matvec4_kernel<K, NT, STEPS>;
-    if (smem > 48 * 1024 && !allow_smem<kSmemLimit>(kern)) return BAKRON_ERR_CUDA;
+    if (smem > 48 * 1024 && !allow_smem<kSmemLimit - kStaticSmem>(kern)) return BAKRON_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.clusters * ck), (unsigned)((a.tokens + a.chunk - 1) / a.chunk));
     cfg.blockDim = dim3(warps_of(K) * 32);
@@ -658,10 +657,13 @@ Cut cut(const Args& a, int ck, int nt, int sms, bool few_tiles) {
     c.pitch = K == kI8 ? row + 32 : row % 128 ? row : row + 64;
     const int tok = nt * tile_tokens(K);
     const size_t limit = kSmemLimit;
+    // What a block takes, the static array at most: its bytes stand for the place of the first warp.
+    const size_t first = (size_t)tok * 16 * 4;
+    static_assert(tile_tokens(K) * 16 * 4 >= kStaticSmem, "a place is no less than the static array");
     const auto bytes = [&] {
         size_t b = (size_t)warps_of(K) * kStages * (kBatch * 512 + a.batch_groups * 64) +
                    (size_t)c.chunk * token_rows(K) * c.pitch +
-                   (size_t)tok * 16 * 4 * (c.max_tiles + warps_of(K) - 1) + warps_of(K) * 4;
+                   (size_t)tok * 16 * 4 * (c.max_tiles + warps_of(K));
         if (is_book(K)) b += planes(K) * 32768;
         if (a.Gx > 1) b += (size_t)tok * 4 * ((size_t)c.slice * 64 / a.gx + 2);
         return b;
@@ -687,8 +689,8 @@ Cut cut(const Args& a, int ck, int nt, int sms, bool few_tiles) {
             c.max_tiles = (P.mt + c.clusters - 1) / c.clusters;
             // sums of at most 64 row tiles stay in shared memory: more clusters than fit at once
             if (c.max_tiles > 64) c.max_tiles = 64, c.clusters = (P.mt + 63) / 64;
-            c.smem = bytes();
-            if (occ * (c.smem + 1024) <= 228 * 1024 && c.smem <= limit) {
+            if (occ * (bytes() + 1024) <= 228 * 1024 && bytes() <= limit) {
+                c.smem = bytes() - first;
                 taken();
                 return c;
             }
@@ -703,7 +705,7 @@ Cut cut(const Args& a, int ck, int nt, int sms, bool few_tiles) {
         if (c.max_tiles < 1) continue;
         c.clusters = (P.mt + c.max_tiles - 1) / c.max_tiles;
         c.max_tiles = (P.mt + c.clusters - 1) / c.clusters;
-        c.smem = bytes();
+        c.smem = bytes() - first;
         taken();
         return c;
     }
