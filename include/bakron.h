@@ -331,10 +331,13 @@ int bakron_unpack4(const void* packed, int m, int n, int group_size, int unsigne
  * v(code) is the code itself or, with a codebook, its entry. 8-bit activations stand for
  * x_scales[t][j / x_group_size] * x[t][j]. Products are exact or carried to 22 bits and more
  * (fp32 activations: 24 bits; with a codebook: entries to 22 bits for fp16 and 8-bit
- * activations, 24 for fp32, for bf16 24 with an fp32 result and 16 with a 16-bit one), sums are fp32 (8-bit activations on the integer grid:
- * exact within 64 columns), and the result is rounded once to y's type.
- * Any number of tokens is right; the weights are read once for up to 32 tokens (8 tokens of fp32;
- * fewer in layers of very long rows), so it is meant for few.
+ * activations, 24 for fp32, for bf16 24 with an fp32 result and 16 with a 16-bit one), sums are
+ * fp32 (8-bit activations on the integer grid: exact within 64 columns), and the result is rounded
+ * once to y's type.
+ * Any number of tokens is right, but it is meant for few: one reading of the weights serves at most
+ * 32 tokens (8 of fp32), and fewer the larger the layer is, for activations and sums share a block's
+ * memory. 28672 x 8192 with group_size 128: 16 tokens of bf16 or fp16, 23 of int8, 8 of fp32; with a
+ * codebook 8 (fp32 4). 4096 x 4096: 32, 32 and 8; with a codebook 25 (fp32 8).
  *
  *   packed, m, n, group_size [in] as for bakron_pack4.
  *   codebook [in]  HOST pointer to 2^bits finite entries, copied during the call (the codes are
@@ -411,7 +414,8 @@ int bakron_rms_norm_q8(const void* x, int64_t ldx, const void* residual, int64_t
  *   dev_status [out] BAKRON_ERR_INVALID_ARG if an index is >= vocab (that entry counts as
  *                  absent).
  * Logits of -inf are entries of probability 0; a NaN, a +inf, or a row of nothing but -inf gives
- * a row with a present entry a NaN loss and gradient.
+ * a row with a present entry a NaN loss and gradient. An entry whose p_j is 0 in fp32 adds nothing to
+ * either, and a row of nothing but such entries is like one without a present entry.
  * ---------------------------------------------------------------------------------------- */
 int bakron_distill(const void* logits, int dtype, int rows, int vocab, int64_t ld,
                    const void* top_idx, int idx_dtype, const void* top_logits, int top_dtype,

@@ -9,8 +9,8 @@
 // multiply-add on the CUDA cores would need an unpacked fp32 factor and one instruction a weight
 // and token. The legacy tensor path (mma.sync m16n8k16 / k32) takes both factors in 16 or 8 bits
 // from registers and multiplies 8 columns at once: one token leaves most of it idle, eight cost the
-// same. (tcgen05.mma would want the unpacked weights in shared memory first: two more passes over
-// them there, for products that are not what bounds this kernel.)
+// same. (tcgen05.mma takes them from shared or tensor memory, where they would have to be put first, one
+// more write and read of every weight for products that are not what bounds a few tokens.)
 //
 //   * A warp owns a row tile (16 rows) and a slice of the columns. Each lane's 16 bytes of a 512-byte
 //     tile are its own fragments of four m16n8k16 (two m16n8k32) products. A warp copies its tiles
@@ -32,7 +32,8 @@
 //
 // Measured, 28672 x 8192, group 128 (19.3 us at the measured copy rate): one token of bf16 29.1, fp16
 // 26.5, int8 25.1 (5.0 TB/s), fp32 32.2 us; 8 bf16 tokens 32.5, 16 tokens 45.5, 32 tokens 97.2; with a
-// codebook 50 to 52 (fp32 70), where the table's reads fill shared memory's data path.
+// codebook 50 to 52 (fp32 70, fp32 results of bf16 64), where the table's reads fill shared memory's
+// data path. With four product tiles most instantiations spill 12 to 72 bytes a thread (128 registers).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -139,9 +140,10 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t 
     return r;
 }
 
-// The 8 codes of a word as four f16 pairs: columns (0, 1), (2, 3), (4, 5), (6, 7). The xor turns
-// the two's complement nibble into code + 8 under the exponent of 1024 (or 64 for the upper
-// nibble, with the product by 1/16).
+// The 8 codes of a word as four f16 pairs: columns (0, 1), (2, 3), (4, 5), (6, 7). Integers become
+// floating point by setting exponent bits around them, as published by Kim et al., 2022 ("Who Says
+// Elephants Can't Run"): the xor turns the two's complement nibble into code + 8 under the exponent
+// of 1024 (or 64 for the upper nibble, with the product by 1/16).
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&p)[4]) {
     const __half2 c0 = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));
     const __half2 c1 = __floats2half2_rn(-72.f, -72.f), r16 = __floats2half2_rn(0.0625f, 0.0625f);
@@ -677,8 +679,8 @@ Cut cut(const Args& a, int ck, int nt, int sms, bool few_tiles) {
                                    0.08 * c.slice * c.chunk * token_rows(K) + 4.0);
     };
     c.chunk = std::min(a.tokens, tok);
-    // SMs that clusters of ck blocks can fill (they do not cross a GPC): 132 of 148 in fours, 120 in
-    // eights, as the occupancy query says; one more would wait for a second wave
+    // SMs that clusters of ck blocks can fill (they do not cross a GPC): on a B200 132 of 148 in fours,
+    // 120 in eights, as its occupancy query says; one more would wait for a second wave
     const int fit = ck <= 2 ? sms : ck == 4 ? sms * 33 / 37 : sms * 30 / 37;
     // blocks an SM and row tiles a cluster depend on each other through shared memory: from the
     // most blocks down to what fits

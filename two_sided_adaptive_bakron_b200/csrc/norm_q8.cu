@@ -18,9 +18,10 @@
 // within 2^-14 of the border of two codes, one element in 8000 -- fp64 decides, with the group's
 // maximum in fp64; the products of 16-bit inputs are exact there.
 //
-// Measured: 2048 x 8192 bf16 with a residual, groups of 128: 34.0 us (3.5 TB/s; 36 instructions an
-// element, so bound by those), one group a row 42.8; fp32 45.8 (4.8 TB/s). Blocks of 128 threads for
-// groups within a warp: 33.3 us, of 256 35.1, of 384 41.3, of 512 54.6.
+// Measured: 2048 x 8192 bf16 with a residual, groups of 128: 34.0 us (3.5 TB/s; issue 62%, DRAM 30%: no
+// unit is at its limit, but a block has only one round of loads on its way ahead), one group a row 42.8;
+// fp32 45.8 (4.8 TB/s). Blocks of 128 threads for groups within a warp: 33.3 us, of 256 35.1, of 384
+// 41.3, of 512 54.6.
 #include <cmath>
 
 #include "lowp.cuh"
